@@ -304,6 +304,29 @@ typedef struct {
 moe_status moe_forward_workspace_layout(const moe_shape* shape, moe_workspace_layout* layout);
 
 /* ----------------------------------------------------------------------------
+ * moe_decode - the whole layer for a few tokens (a serving step: one new token for each of
+ * up to MOE_DECODE_MAX_TOKENS requests), in two kernels: the router, then both expert
+ * products and the combine in one persistent kernel bound by reading each taken expert's
+ * weights once. The pages have no counterpart (a deployment variant of moe_forward).
+ * Computes what moe_forward computes, with the expert outputs kept in fp32 until the
+ * combine (moe_forward rounds them to bf16 between its kernels):
+ *   out[t] = sum_k w[t,k] (silu(x_t W_gate[e]) * (x_t W_up[e])) W_down[e],  e = id[t,k].
+ * Arguments, ties, renormalize, bias, logits_in and capacity_factor as moe_forward; a row of
+ * x or logits that is NaN, or logits that are all -inf, give a NaN row and touch no other.
+ * Results repeat bit for bit. ffn_variant and route_topk do not apply.
+ * bf16 only; T <= MOE_DECODE_MAX_TOKENS; no tile_round: else MOE_ERR_UNSUPPORTED.
+ * x, w_r, w_gate, w_up, w_down and out 16-byte aligned, workspace 256-byte aligned and
+ * >= moe_decode_workspace_size(shape); nothing in it has to be set before a call or kept
+ * after it. Calls that may run at the same time need a workspace each.
+ */
+#define MOE_DECODE_MAX_TOKENS 128
+size_t moe_decode_workspace_size(const moe_shape* shape);
+moe_status moe_decode(const moe_shape* shape, const void* x, const void* w_r, const float* bias,
+                      const float* logits_in, const void* w_gate, const void* w_up,
+                      const void* w_down, void* out, void* workspace, size_t ws_bytes,
+                      moe_stream_t stream);
+
+/* ----------------------------------------------------------------------------
  * moe_forward_h - moe_forward that also keeps, for the backward, the gate/up
  * pre-activations of every kept slot: h [T*K, 2n] bf16, row p = (g | u) with
  * g = x[tok(p)] W_gate[e], u = x[tok(p)] W_up[e] (rows past offsets[E] unwritten).

@@ -75,6 +75,8 @@ _SIGS = {
     "moe_forward": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_forward_h": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                      ctypes.c_size_t, _P]),
+    "moe_decode_workspace_size": (ctypes.c_size_t, [_S]),
+    "moe_decode": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_backward_workspace_size": (ctypes.c_size_t, [_S]),
     "moe_backward_router": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_backward": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
@@ -157,6 +159,20 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> None:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _current(t: torch.Tensor, name: str) -> torch.device:
+    """The device of `t`, which has to be the current one (the library launches there)."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _on(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    _dev(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _act_dtype(shape: moe_shape):
@@ -376,6 +392,47 @@ def forward(shape: moe_shape, x, w_r, w_gate, w_up, w_down, bias=None, logits_in
     _check(lib.moe_forward(ctypes.byref(shape), _ptr(x), _ptr(w_r), _ptr(bias), _ptr(logits_in),
                            _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out), _ptr(workspace),
                            workspace.numel(), _stream()), "moe_forward")
+    return out, workspace
+
+
+DECODE_MAX_TOKENS = 128
+
+
+def decode_workspace_size(shape: moe_shape) -> int:
+    return int(load_library().moe_decode_workspace_size(ctypes.byref(shape)))
+
+
+def decode(shape: moe_shape, x, w_r, w_gate, w_up, w_down, bias=None, logits_in=None, out=None,
+           workspace=None):
+    """moe_decode (the whole layer for at most DECODE_MAX_TOKENS tokens, bf16).
+    Returns (out [T, d], workspace)."""
+    lib = load_library()
+    T, d, E, n = shape.T, shape.d, shape.E, shape.n
+    need = decode_workspace_size(shape)
+    if need == 0:
+        raise MoEError(lib.moe_decode(ctypes.byref(shape), *[None] * 9, 0, None), "moe_decode")
+    _dev(x, "x", torch.bfloat16, (T, d))
+    dev = _current(x, "x")
+    if logits_in is None:
+        _on(w_r, "w_r", torch.bfloat16, (d, E), dev)
+    else:
+        _on(logits_in, "logits_in", torch.float32, (T, E), dev)
+    _on(w_gate, "w_gate", torch.bfloat16, (E, d, n), dev)
+    _on(w_up, "w_up", torch.bfloat16, (E, d, n), dev)
+    _on(w_down, "w_down", torch.bfloat16, (E, n, d), dev)
+    if bias is not None:
+        _on(bias, "bias", torch.float32, (E,), dev)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _on(workspace, "workspace", torch.uint8, None, dev)
+    if out is None:
+        out = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
+    else:
+        _on(out, "out", torch.bfloat16, (T, d), dev)
+    _check(lib.moe_decode(ctypes.byref(shape), _ptr(x), _ptr(w_r), _ptr(bias), _ptr(logits_in),
+                          _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out), _ptr(workspace),
+                          workspace.numel(), _stream()), "moe_decode")
     return out, workspace
 
 

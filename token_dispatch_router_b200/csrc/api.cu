@@ -66,6 +66,12 @@ moe_status launch_combine_added(const moe_shape& s, const void* y_perm, const in
                                 const int32_t* add_idx, const float* add_w, long long n_rows,
                                 cudaStream_t st);
 
+size_t decode_workspace_bytes(const moe_shape& s);
+moe_status launch_decode(const moe_shape& s, const void* x, const void* w_r, const float* bias,
+                         const float* logits_in, const void* w_gate, const void* w_up,
+                         const void* w_down, void* out, int cap, uint8_t* ws,
+                         cudaStream_t st);
+
 // Rounding up or to the nearest tile: added assignments beyond T * K.
 bool rounds_up(const moe_shape& s) { return s.tile_round > 1 && s.tile_round_mode != 0; }
 // The permutation over the extended assignment list runs as T * K + E * (R - 1)
@@ -125,7 +131,8 @@ const char* kKernelNames[K_COUNT] = {
     "route_tc",     "permute_small", "gateup_tc2",   "down_tc2",
     "permute_cluster", "tile_round", "bwd_act", "bwd_dw", "bwd_dx",
     "router_dlogits", "router_dwr", "router_dx", "omni_logits", "omni_topk", "omni_count",
-    "omni_scan", "omni_scatter", "omni_sort", "omni_act", "omni_out"};
+    "omni_scan", "omni_scatter", "omni_sort", "omni_act", "omni_out", "decode_route", "decode",
+    "adapter_few"};
 
 struct ProfRec {
   int kid;
@@ -608,6 +615,43 @@ moe_status moe_backward_router(const moe_shape* s, const void* x, const void* w_
   if (s->E > 16 && !aligned16(x)) return MOE_ERR_INVALID_ARG;  // 16-byte row loads of x
   return launch_router_backward(*s, x, w_r, logits, topk_ids, topk_w, d_w, d_logits, d_w_r,
                                 d_bias, d_x, (cudaStream_t)stream);
+}
+
+// Kept assignments per expert of at most 128 tokens (T when there is no limit).
+static int decode_capacity(const moe_shape& s) {
+  if (!(s.capacity_factor > 0.f)) return s.T;
+  const double c = ceil((double)s.capacity_factor * (double)s.T * (double)s.K / (double)s.E);
+  return c < (double)s.T ? (int)c : s.T;
+}
+
+static moe_status check_decode(const moe_shape* s) {
+  const moe_status r = check_shape(s, true, true);
+  if (r != MOE_OK) return r;
+  if (s->dtype != MOE_BF16 || s->T > MOE_DECODE_MAX_TOKENS || s->tile_round > 0)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_decode_workspace_size(const moe_shape* s) {
+  if (check_decode(s) != MOE_OK) return 0;
+  return decode_workspace_bytes(*s);
+}
+
+moe_status moe_decode(const moe_shape* s, const void* x, const void* w_r, const float* bias,
+                      const float* logits_in, const void* w_gate, const void* w_up,
+                      const void* w_down, void* out, void* workspace, size_t ws_bytes,
+                      moe_stream_t stream) {
+  const moe_status r = check_decode(s);
+  if (r != MOE_OK) return r;
+  if (s->T == 0) return MOE_OK;
+  if (!x || (!w_r && !logits_in) || !w_gate || !w_up || !w_down || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || (!logits_in && !aligned16(w_r)) || !aligned16(w_gate) ||
+      !aligned16(w_up) || !aligned16(w_down) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  if (workspace == nullptr || ws_bytes < decode_workspace_bytes(*s)) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)workspace & 255) != 0) return MOE_ERR_INVALID_ARG;
+  return launch_decode(*s, x, w_r, bias, logits_in, w_gate, w_up, w_down, out,
+                       decode_capacity(*s), (uint8_t*)workspace, (cudaStream_t)stream);
 }
 
 moe_status moe_get_device_status(moe_stream_t stream) {

@@ -37,6 +37,9 @@ enum KernelId {
   K_OMNI_SORT,
   K_OMNI_ACT,
   K_OMNI_OUT,
+  K_DECODE_ROUTE,
+  K_DECODE,
+  K_ADAPTER_FEW,
   K_COUNT
 };
 
