@@ -327,6 +327,54 @@ moe_status moe_decode(const moe_shape* shape, const void* x, const void* w_r, co
                       moe_stream_t stream);
 
 /* ----------------------------------------------------------------------------
+ * moe_adapter_forward, moe_adapter_backward - a dense projection that all requests share (an
+ * attention output or a shared feed-forward projection beside the experts) with a low-rank
+ * adapter of its own for each request's rows. The pages have no counterpart; rows are grouped
+ * by adapter as moe_permute groups them by expert. For row t with l = ids[t]:
+ *     low[t] = scale[l] x_t A[l]                  (fp32; 0 without an adapter)
+ *     y_t    = x_t W + low[t] B[l]                (fp32 sums, rounded once to bf16)
+ * and, with W held fixed,
+ *     d_low  = scale[l] d_y_t B[l]^T              (fp32)
+ *     d_x_t  = d_y_t W^T + d_low A[l]^T           (fp32 sums, rounded once to bf16)
+ *     d_a[l] = sum over l's rows of x_t^T d_low,  d_b[l] = sum of low[t]^T d_y_t   (fp32)
+ * Results repeat bit for bit. Adapters do not mix: an infinity or NaN of one adapter, or of
+ * one row, stays in the rows (and, backward, the gradients) that it belongs to.
+ *
+ *   x     [T, d_in]  w [d_in, d_out]  a [n_adapters, d_in, rank]  b [n_adapters, rank, d_out]
+ *         device bf16
+ *   ids   [T]           device int32: the adapter of each row, -1 for none (another value
+ *                       outside [0, n_adapters) counts as none and flags
+ *                       MOE_ERR_DEVICE_INDEX)
+ *   scale [n_adapters]  device fp32
+ *   low   [T, rank]     device fp32: forward out, backward in
+ *   y     [T, d_out]    device bf16 out;  d_y [T, d_out] device bf16
+ *   d_x   [T, d_in]     device bf16 out, or NULL (w may then be NULL)
+ *   d_a, d_b            device fp32 out, shaped as a and b; all written (zeros for an adapter
+ *                       that no row uses)
+ * d_in and d_out multiples of 64, rank a multiple of 8, else MOE_ERR_INVALID_ARG; bf16 only,
+ * rank <= 128, n_adapters <= 256, T <= 2^24, else MOE_ERR_UNSUPPORTED. Adapters of several
+ * ranks: the largest one, the others padded with zeros. Every pointer except ids and scale
+ * 16-byte aligned; workspace 256-byte aligned, >= moe_adapter_workspace_size(shape), nothing
+ * in it has to be set before a call or kept after it. Calls that may run at the same time need
+ * a workspace each. T = 0: forward does nothing, backward zeroes d_a and d_b.
+ */
+typedef struct {
+  int32_t T, d_in, d_out, n_adapters, rank;
+  int32_t dtype; /* moe_dtype */
+} moe_adapter_shape;
+
+size_t moe_adapter_workspace_size(const moe_adapter_shape* shape);
+moe_status moe_adapter_forward(const moe_adapter_shape* shape, const void* x, const void* w,
+                               const void* a, const void* b, const int32_t* ids,
+                               const float* scale, float* low, void* y, void* workspace,
+                               size_t ws_bytes, moe_stream_t stream);
+moe_status moe_adapter_backward(const moe_adapter_shape* shape, const void* d_y, const void* x,
+                                const void* w, const void* a, const void* b, const int32_t* ids,
+                                const float* scale, const float* low, void* d_x, float* d_a,
+                                float* d_b, void* workspace, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/* ----------------------------------------------------------------------------
  * moe_forward_h - moe_forward that also keeps, for the backward, the gate/up
  * pre-activations of every kept slot: h [T*K, 2n] bf16, row p = (g | u) with
  * g = x[tok(p)] W_gate[e], u = x[tok(p)] W_up[e] (rows past offsets[E] unwritten).

@@ -46,6 +46,11 @@ class moe_workspace_layout(ctypes.Structure):
         "total")]
 
 
+class moe_adapter_shape(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("T", "d_in", "d_out", "n_adapters", "rank",
+                                              "dtype")]
+
+
 class moe_omni_shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("n_rows", ctypes.c_int32),
                 ("n_cols", ctypes.c_int32), ("K", ctypes.c_int32),
@@ -61,6 +66,7 @@ class moe_omni_layout(ctypes.Structure):
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(moe_shape)
 _O = ctypes.POINTER(moe_omni_shape)
+_A = ctypes.POINTER(moe_adapter_shape)
 _SIGS = {
     "moe_permute_workspace_size": (ctypes.c_size_t, [_S]),
     "moe_forward_workspace_size": (ctypes.c_size_t, [_S]),
@@ -77,6 +83,11 @@ _SIGS = {
                                      ctypes.c_size_t, _P]),
     "moe_decode_workspace_size": (ctypes.c_size_t, [_S]),
     "moe_decode": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_adapter_workspace_size": (ctypes.c_size_t, [_A]),
+    "moe_adapter_forward": (ctypes.c_int, [_A, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                           ctypes.c_size_t, _P]),
+    "moe_adapter_backward": (ctypes.c_int, [_A, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                            ctypes.c_size_t, _P]),
     "moe_backward_workspace_size": (ctypes.c_size_t, [_S]),
     "moe_backward_router": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_backward": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
@@ -434,6 +445,100 @@ def decode(shape: moe_shape, x, w_r, w_gate, w_up, w_down, bias=None, logits_in=
                           _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out), _ptr(workspace),
                           workspace.numel(), _stream()), "moe_decode")
     return out, workspace
+
+
+def make_adapter_shape(T: int, d_in: int, d_out: int, n_adapters: int, rank: int,
+                       dtype=torch.bfloat16) -> moe_adapter_shape:
+    """T rows through a shared [d_in, d_out] projection with n_adapters adapters of one rank."""
+    return moe_adapter_shape(T, d_in, d_out, n_adapters, rank,
+                             MOE_BF16 if dtype == torch.bfloat16 else MOE_F32)
+
+
+def adapter_workspace_size(shape: moe_adapter_shape) -> int:
+    return int(load_library().moe_adapter_workspace_size(ctypes.byref(shape)))
+
+
+def _adapter_workspace(shape: moe_adapter_shape, workspace, dev):
+    need = adapter_workspace_size(shape)
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _on(workspace, "workspace", torch.uint8, None, dev)
+    return workspace
+
+
+def _check_adapter_shape(shape: moe_adapter_shape, where: str) -> None:
+    lib = load_library()
+    if lib.moe_adapter_workspace_size(ctypes.byref(shape)) == 0:
+        raise MoEError(lib.moe_adapter_forward(ctypes.byref(shape), *[None] * 9, 0, None), where)
+
+
+def adapter_forward(shape: moe_adapter_shape, x, w, a, b, ids, scale, low=None, out=None,
+                    workspace=None):
+    """moe_adapter_forward: x W + scale[l] (x A[l]) B[l] with l = ids[row], -1 for none.
+    Returns (y [T, d_out] bf16, low [T, rank] fp32, workspace); the backward reads low."""
+    _check_adapter_shape(shape, "moe_adapter_forward")
+    T, d_in, d_out, L, r = (shape.T, shape.d_in, shape.d_out, shape.n_adapters, shape.rank)
+    bf = torch.bfloat16
+    _dev(x, "x", bf, (T, d_in))
+    dev = _current(x, "x")
+    _on(w, "w", bf, (d_in, d_out), dev)
+    _on(a, "a", bf, (L, d_in, r), dev)
+    _on(b, "b", bf, (L, r, d_out), dev)
+    _on(ids, "ids", torch.int32, (T,), dev)
+    _on(scale, "scale", torch.float32, (L,), dev)
+    if low is None:
+        low = torch.empty(T, r, dtype=torch.float32, device=dev)
+    else:
+        _on(low, "low", torch.float32, (T, r), dev)
+    if out is None:
+        out = torch.empty(T, d_out, dtype=bf, device=dev)
+    else:
+        _on(out, "out", bf, (T, d_out), dev)
+    workspace = _adapter_workspace(shape, workspace, dev)
+    _check(load_library().moe_adapter_forward(
+        ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(a), _ptr(b), _ptr(ids), _ptr(scale),
+        _ptr(low), _ptr(out), _ptr(workspace), workspace.numel(), _stream()),
+        "moe_adapter_forward")
+    return out, low, workspace
+
+
+def adapter_backward(shape: moe_adapter_shape, d_y, x, w, a, b, ids, scale, low, d_x=None,
+                     d_a=None, d_b=None, want_d_x: bool = True, workspace=None):
+    """moe_adapter_backward (w held fixed); low from adapter_forward on the same arguments.
+    Returns (d_x [T, d_in] bf16 or None, d_a [L, d_in, r] fp32, d_b [L, r, d_out] fp32)."""
+    _check_adapter_shape(shape, "moe_adapter_backward")
+    T, d_in, d_out, L, r = (shape.T, shape.d_in, shape.d_out, shape.n_adapters, shape.rank)
+    bf, f32 = torch.bfloat16, torch.float32
+    _dev(d_y, "d_y", bf, (T, d_out))
+    dev = _current(d_y, "d_y")
+    _on(x, "x", bf, (T, d_in), dev)
+    if want_d_x:
+        _on(w, "w", bf, (d_in, d_out), dev)
+        if d_x is None:
+            d_x = torch.empty(T, d_in, dtype=bf, device=dev)
+        else:
+            _on(d_x, "d_x", bf, (T, d_in), dev)
+    elif d_x is not None:
+        raise ValueError("d_x was given, but want_d_x is False")
+    _on(a, "a", bf, (L, d_in, r), dev)
+    _on(b, "b", bf, (L, r, d_out), dev)
+    _on(ids, "ids", torch.int32, (T,), dev)
+    _on(scale, "scale", f32, (L,), dev)
+    _on(low, "low", f32, (T, r), dev)
+    if d_a is None:
+        d_a = torch.empty(L, d_in, r, dtype=f32, device=dev)
+    else:
+        _on(d_a, "d_a", f32, (L, d_in, r), dev)
+    if d_b is None:
+        d_b = torch.empty(L, r, d_out, dtype=f32, device=dev)
+    else:
+        _on(d_b, "d_b", f32, (L, r, d_out), dev)
+    workspace = _adapter_workspace(shape, workspace, dev)
+    _check(load_library().moe_adapter_backward(
+        ctypes.byref(shape), _ptr(d_y), _ptr(x), _ptr(w if want_d_x else None), _ptr(a), _ptr(b),
+        _ptr(ids), _ptr(scale), _ptr(low), _ptr(d_x), _ptr(d_a), _ptr(d_b), _ptr(workspace),
+        workspace.numel(), _stream()), "moe_adapter_backward")
+    return d_x, d_a, d_b
 
 
 def forward_h(shape: moe_shape, x, w_r, w_gate, w_up, w_down, bias=None, logits_in=None,

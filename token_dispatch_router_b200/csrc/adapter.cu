@@ -1,0 +1,175 @@
+// Host side of the adapter products: workspace layouts and launch sequences.
+//
+//   forward,  at most 128 rows: low partials -> the few-token product kernel (two launches)
+//   forward,  more rows:        group rows by adapter -> low -> product with the adapter term
+//   backward:                   group -> d_low -> d_x product with the adapter term
+//                               -> outer products d_A, d_B
+// Grouping is the layer's stable permutation with one "expert" an adapter and K = 1; a row
+// with id -1 belongs to none.
+#include "few.cuh"
+
+namespace moe {
+
+size_t permute_scratch_bytes(const moe_shape& s);
+moe_status launch_permute(const moe_shape& s, const int32_t* ids, int32_t* counts,
+                          int32_t* offsets, int32_t* a2p, int32_t* p2a, const void* x,
+                          void* x_perm, void* scratch, cudaStream_t st);
+int adapter_few_splits(int T, int d_out);
+moe_status launch_adapter_few(int T, int d_in, int d_out, int n_adapters, int rank, const void* x,
+                              const void* w, const void* b, const int32_t* ids,
+                              const float* scale, const float* low_part, int low_splits,
+                              float* low, void* y, float* y32, int smax, uint32_t* ctl,
+                              cudaStream_t st);
+moe_status launch_adapter_low_few(int T, int D, int r, int L, int splits, const void* x,
+                                  const void* a, const int32_t* ids, float* part,
+                                  uint32_t* clear, int n_clear, cudaStream_t st);
+moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void* in,
+                              const void* m, const int32_t* ids, const int32_t* offsets,
+                              const int32_t* rows, const float* scale, float* low, void* planes,
+                              const float* low2, void* planes2, uint32_t* clear, int n_clear,
+                              cudaStream_t st);
+moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
+                               const void* in, const void* w, const int32_t* ids,
+                               const float* low, const void* w2, void* out, cudaStream_t st);
+size_t adapter_outer_part_bytes(int T, int d_in, int d_out, int r);
+size_t adapter_outer_arrived_words(int d_in, int d_out, int L);
+moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
+                                const void* d_y, const void* planes_d_low,
+                                const void* planes_low, const int32_t* offsets,
+                                const int32_t* rows, float* d_a, float* d_b, float* part,
+                                uint32_t* arrived, cudaStream_t st);
+
+namespace {
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Splits of the few-row low sums: two CTAs a SM over all rows, at least 64 of d_in each.
+int low_few_splits(const moe_adapter_shape& s) {
+  int n = 2 * 148 / (s.T > 0 ? s.T : 1);
+  if (n > s.d_in / 64) n = s.d_in / 64;
+  return n < 1 ? 1 : n > 16 ? 16 : n;
+}
+
+moe_shape group_shape(const moe_adapter_shape& s) {
+  moe_shape g = {};
+  g.T = s.T;
+  g.d = 64;
+  g.E = s.n_adapters;
+  g.K = 1;
+  g.dtype = MOE_BF16;
+  return g;
+}
+
+struct FewLayout {
+  size_t ctl, low_part, y32, total;
+  int smax;
+};
+FewLayout few_layout(const moe_adapter_shape& s) {
+  FewLayout L;
+  size_t o = 0;
+  L.ctl = o;
+  o = up256(o + kFewCtlWords * 4);
+  L.low_part = o;
+  o = up256(o + (size_t)low_few_splits(s) * s.T * s.rank * 4);
+  L.y32 = o;
+  L.smax = adapter_few_splits(s.T, s.d_out);
+  o = up256(o + (size_t)L.smax * s.T * s.d_out * 4);
+  L.total = o;
+  return L;
+}
+
+struct Layout {
+  size_t counts, offsets, a2p, rows, scratch;                    // grouping
+  size_t d_low, planes_d, planes_l, arrived, part, total_fwd, total;  // backward
+};
+Layout layout(const moe_adapter_shape& s) {
+  Layout L;
+  const size_t T = s.T, r = s.rank;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = up256(o + bytes);
+    return at;
+  };
+  L.counts = take((size_t)s.n_adapters * 4);
+  L.offsets = take(((size_t)s.n_adapters + 1) * 4);
+  L.a2p = take(T * 4);
+  L.rows = take(T * 4);
+  L.scratch = take(permute_scratch_bytes(group_shape(s)));
+  L.total_fwd = o;
+  L.d_low = take(T * r * 4);
+  L.planes_d = take(3 * T * r * 2);
+  L.planes_l = take(3 * T * r * 2);
+  L.arrived = take(adapter_outer_arrived_words(s.d_in, s.d_out, s.n_adapters) * 4);
+  L.part = take(adapter_outer_part_bytes(s.T, s.d_in, s.d_out, s.rank));
+  L.total = o;
+  return L;
+}
+
+moe_status group(const moe_adapter_shape& s, const int32_t* ids, const Layout& L, uint8_t* ws,
+                 cudaStream_t st) {
+  return launch_permute(group_shape(s), ids, (int32_t*)(ws + L.counts),
+                        (int32_t*)(ws + L.offsets), (int32_t*)(ws + L.a2p),
+                        (int32_t*)(ws + L.rows), nullptr, nullptr, ws + L.scratch, st);
+}
+
+}  // namespace
+
+size_t adapter_forward_bytes(const moe_adapter_shape& s) {
+  return s.T <= kFewMaxTokens ? few_layout(s).total : layout(s).total_fwd;
+}
+size_t adapter_backward_bytes(const moe_adapter_shape& s) { return layout(s).total; }
+
+moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, const void* w,
+                                  const void* a, const void* b, const int32_t* ids,
+                                  const float* scale, float* low, void* y, uint8_t* ws,
+                                  cudaStream_t st) {
+  moe_status r;
+  if (s.T <= kFewMaxTokens) {
+    const FewLayout L = few_layout(s);
+    const int splits = low_few_splits(s);
+    uint32_t* ctl = (uint32_t*)(ws + L.ctl);
+    float* part = (float*)(ws + L.low_part);
+    if ((r = launch_adapter_low_few(s.T, s.d_in, s.rank, s.n_adapters, splits, x, a, ids, part,
+                                    ctl, kFewCtlWords, st)) != MOE_OK)
+      return r;
+    return launch_adapter_few(s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w, b, ids, scale,
+                              part, splits, low, y, (float*)(ws + L.y32), L.smax, ctl, st);
+  }
+  const Layout L = layout(s);
+  if ((r = group(s, ids, L, ws, st)) != MOE_OK) return r;
+  if ((r = launch_adapter_low(false, s.T, s.d_in, s.rank, s.n_adapters, x, a, ids,
+                              (const int32_t*)(ws + L.offsets), (const int32_t*)(ws + L.rows),
+                              scale, low, nullptr, nullptr, nullptr, nullptr, 0, st)) != MOE_OK)
+    return r;
+  return launch_adapter_gemm(false, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w, ids, low, b,
+                             y, st);
+}
+
+moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, const void* x,
+                                   const void* w, const void* a, const void* b,
+                                   const int32_t* ids, const float* scale, const float* low,
+                                   void* d_x, float* d_a, float* d_b, uint8_t* ws,
+                                   cudaStream_t st) {
+  const Layout L = layout(s);
+  const int32_t* offsets = (const int32_t*)(ws + L.offsets);
+  const int32_t* rows = (const int32_t*)(ws + L.rows);
+  float* d_low = (float*)(ws + L.d_low);
+  uint32_t* arrived = (uint32_t*)(ws + L.arrived);
+  moe_status r;
+  if ((r = group(s, ids, L, ws, st)) != MOE_OK) return r;
+  if ((r = launch_adapter_low(
+           true, s.T, s.d_out, s.rank, s.n_adapters, d_y, b, ids, offsets, rows, scale, d_low,
+           ws + L.planes_d, low, ws + L.planes_l, arrived,
+           (int)adapter_outer_arrived_words(s.d_in, s.d_out, s.n_adapters), st)) != MOE_OK)
+    return r;
+  if (d_x != nullptr &&
+      (r = launch_adapter_gemm(true, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, d_y, w, ids,
+                               d_low, a, d_x, st)) != MOE_OK)
+    return r;
+  return launch_adapter_outer(s.T, s.d_in, s.d_out, s.rank, s.n_adapters, x, d_y,
+                              ws + L.planes_d, ws + L.planes_l, offsets, rows, d_a, d_b,
+                              (float*)(ws + L.part), arrived, st);
+}
+
+}  // namespace moe

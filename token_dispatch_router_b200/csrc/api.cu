@@ -72,6 +72,18 @@ moe_status launch_decode(const moe_shape& s, const void* x, const void* w_r, con
                          const void* w_down, void* out, int cap, uint8_t* ws,
                          cudaStream_t st);
 
+size_t adapter_forward_bytes(const moe_adapter_shape& s);
+size_t adapter_backward_bytes(const moe_adapter_shape& s);
+moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, const void* w,
+                                  const void* a, const void* b, const int32_t* ids,
+                                  const float* scale, float* low, void* y, uint8_t* ws,
+                                  cudaStream_t st);
+moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, const void* x,
+                                   const void* w, const void* a, const void* b,
+                                   const int32_t* ids, const float* scale, const float* low,
+                                   void* d_x, float* d_a, float* d_b, uint8_t* ws,
+                                   cudaStream_t st);
+
 // Rounding up or to the nearest tile: added assignments beyond T * K.
 bool rounds_up(const moe_shape& s) { return s.tile_round > 1 && s.tile_round_mode != 0; }
 // The permutation over the extended assignment list runs as T * K + E * (R - 1)
@@ -132,7 +144,7 @@ const char* kKernelNames[K_COUNT] = {
     "permute_cluster", "tile_round", "bwd_act", "bwd_dw", "bwd_dx",
     "router_dlogits", "router_dwr", "router_dx", "omni_logits", "omni_topk", "omni_count",
     "omni_scan", "omni_scatter", "omni_sort", "omni_act", "omni_out", "decode_route", "decode",
-    "adapter_few"};
+    "adapter_few",  "adapter_low_few", "adapter_low", "adapter_gemm", "adapter_outer"};
 
 struct ProfRec {
   int kid;
@@ -652,6 +664,66 @@ moe_status moe_decode(const moe_shape* s, const void* x, const void* w_r, const 
   if (((uintptr_t)workspace & 255) != 0) return MOE_ERR_INVALID_ARG;
   return launch_decode(*s, x, w_r, bias, logits_in, w_gate, w_up, w_down, out,
                        decode_capacity(*s), (uint8_t*)workspace, (cudaStream_t)stream);
+}
+
+static moe_status check_adapter(const moe_adapter_shape* s) {
+  if (s == nullptr) return MOE_ERR_INVALID_ARG;
+  if (s->T < 0 || s->d_in < 64 || s->d_in % 64 != 0 || s->d_out < 64 || s->d_out % 64 != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (s->n_adapters < 1 || s->rank < 8 || s->rank % 8 != 0) return MOE_ERR_INVALID_ARG;
+  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (s->dtype != MOE_BF16 || s->n_adapters > 256 || s->rank > 128 || s->T > (1 << 24))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_adapter_workspace_size(const moe_adapter_shape* s) {
+  if (check_adapter(s) != MOE_OK) return 0;
+  const size_t f = adapter_forward_bytes(*s), b = adapter_backward_bytes(*s);
+  return f > b ? f : b;
+}
+
+moe_status moe_adapter_forward(const moe_adapter_shape* s, const void* x, const void* w,
+                               const void* a, const void* b, const int32_t* ids,
+                               const float* scale, float* low, void* y, void* workspace,
+                               size_t ws_bytes, moe_stream_t stream) {
+  const moe_status r = check_adapter(s);
+  if (r != MOE_OK) return r;
+  if (s->T == 0) return MOE_OK;
+  if (!x || !w || !a || !b || !ids || !scale || !low || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(a) || !aligned16(b) || !aligned16(low) ||
+      !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  if (workspace == nullptr || ws_bytes < adapter_forward_bytes(*s)) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)workspace & 255) != 0) return MOE_ERR_INVALID_ARG;
+  return launch_adapter_forward(*s, x, w, a, b, ids, scale, low, y, (uint8_t*)workspace,
+                                (cudaStream_t)stream);
+}
+
+moe_status moe_adapter_backward(const moe_adapter_shape* s, const void* d_y, const void* x,
+                                const void* w, const void* a, const void* b, const int32_t* ids,
+                                const float* scale, const float* low, void* d_x, float* d_a,
+                                float* d_b, void* workspace, size_t ws_bytes,
+                                moe_stream_t stream) {
+  const moe_status r = check_adapter(s);
+  if (r != MOE_OK) return r;
+  if (!d_a || !d_b) return MOE_ERR_INVALID_ARG;
+  if (s->T == 0) {  // no rows: the gradients of A and B are zero
+    const cudaStream_t st = (cudaStream_t)stream;
+    const size_t per = (size_t)s->n_adapters * s->rank * sizeof(float);
+    if (cudaMemsetAsync(d_a, 0, per * s->d_in, st) != cudaSuccess ||
+        cudaMemsetAsync(d_b, 0, per * s->d_out, st) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (!d_y || !x || !a || !b || !ids || !scale || !low || (d_x && !w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(d_y) || !aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(low) ||
+      !aligned16(d_a) || !aligned16(d_b) || (d_x && (!aligned16(w) || !aligned16(d_x))))
+    return MOE_ERR_INVALID_ARG;
+  if (workspace == nullptr || ws_bytes < adapter_backward_bytes(*s)) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)workspace & 255) != 0) return MOE_ERR_INVALID_ARG;
+  return launch_adapter_backward(*s, d_y, x, w, a, b, ids, scale, low, d_x, d_a, d_b,
+                                 (uint8_t*)workspace, (cudaStream_t)stream);
 }
 
 moe_status moe_get_device_status(moe_stream_t stream) {

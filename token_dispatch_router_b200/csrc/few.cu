@@ -724,4 +724,47 @@ moe_status launch_decode(const moe_shape& s, const void* x, const void* w_r, con
   return run_few<false>(mx, mg, mu, ma, md, a, st);
 }
 
+// y = x W + low B[ids] for at most kFewMaxTokens rows; low_part [low_splits][T][rank] are the
+// partial sums of x A[ids], y32 has room for `smax` partials of [T, d_out].
+int adapter_few_splits(int T, int d_out) { return split_room((size_t)T * d_out * 4); }
+
+moe_status launch_adapter_few(int T, int d_in, int d_out, int n_adapters, int rank, const void* x,
+                              const void* w, const void* b, const int32_t* ids,
+                              const float* scale, const float* low_part, int low_splits,
+                              float* low, void* y, float* y32, int smax, uint32_t* ctl,
+                              cudaStream_t st) {
+  FewArgs a = {};
+  a.T = T;
+  a.K = 1;
+  a.E = 1;
+  a.kb1 = 0;
+  a.kb2 = d_in / BK;
+  a.d = d_out;
+  a.nt2 = (d_out + 255) / 256;
+  a.smax1 = 1;
+  a.smax2 = smax;
+  a.cap = T;
+  a.ids = ids;
+  a.ctl = ctl;
+  a.y32 = y32;
+  a.out = (bf16*)y;
+  a.low_part = low_part;
+  a.low = low;
+  a.b = (const bf16*)b;
+  a.scale = scale;
+  a.rank = rank;
+  a.low_splits = low_splits;
+  a.n_adapters = n_adapters;
+  a.status = device_status_ptr();
+  a.limit_ns = kWaitLimitNs;
+  CUtensorMap mx, mw;
+  const uint32_t wbox[3] = {64, 64, 1}, xbox[2] = {64, 16};
+  const uint64_t k = d_in, n = d_out;
+  const uint64_t wd[3] = {n, k, 1}, ws[2] = {n * 2, k * n * 2};
+  const uint64_t xd[2] = {k, (uint64_t)T}, xs[1] = {k * 2};
+  if (!make_map(&mx, x, 2, xd, xs, xbox) || !make_map(&mw, w, 3, wd, ws, wbox))
+    return MOE_ERR_CUDA;
+  return run_few<true>(mx, mw, mw, mx, mw, a, st);
+}
+
 }  // namespace moe

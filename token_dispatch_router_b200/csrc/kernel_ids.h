@@ -40,6 +40,10 @@ enum KernelId {
   K_DECODE_ROUTE,
   K_DECODE,
   K_ADAPTER_FEW,
+  K_ADAPTER_LOW_FEW,
+  K_ADAPTER_LOW,
+  K_ADAPTER_GEMM,
+  K_ADAPTER_OUTER,
   K_COUNT
 };
 
