@@ -6,6 +6,7 @@
 //                               -> outer products d_A, d_B
 // Grouping is the layer's stable permutation with one "expert" an adapter and K = 1; a row
 // with id -1 belongs to none.
+#include "adapter.cuh"
 #include "few.cuh"
 
 namespace moe {
@@ -26,11 +27,12 @@ moe_status launch_adapter_low_few(int T, int D, int r, int L, int splits, const 
 moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void* in,
                               const void* m, const int32_t* ids, const int32_t* offsets,
                               const int32_t* rows, const float* scale, float* low, void* planes,
-                              const float* low2, void* planes2, uint32_t* clear, int n_clear,
+                              const float* low2, void* planes2, void* terms,
+                              AdapterTile* tiles, uint32_t* clear, int n_clear,
                               cudaStream_t st);
 moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
-                               const void* in, const void* w, const int32_t* ids,
-                               const float* low, const void* w2, void* out, cudaStream_t st);
+                               const void* in, const void* w, const AdapterTile* tiles,
+                               const void* low, const void* m, void* out, cudaStream_t st);
 size_t adapter_outer_part_bytes(int T, int d_in, int d_out, int r);
 size_t adapter_outer_arrived_words(int d_in, int d_out, int L);
 moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
@@ -80,6 +82,7 @@ FewLayout few_layout(const moe_adapter_shape& s) {
 
 struct Layout {
   size_t counts, offsets, a2p, rows, scratch;                    // grouping
+  size_t tiles, terms;                                           // for the large product
   size_t d_low, planes_d, planes_l, arrived, part, total_fwd, total;  // backward
 };
 Layout layout(const moe_adapter_shape& s) {
@@ -96,6 +99,8 @@ Layout layout(const moe_adapter_shape& s) {
   L.a2p = take(T * 4);
   L.rows = take(T * 4);
   L.scratch = take(permute_scratch_bytes(group_shape(s)));
+  L.tiles = take((T + kAdapterTileRows - 1) / kAdapterTileRows * sizeof(AdapterTile));
+  L.terms = take(2 * T * r * 2);
   L.total_fwd = o;
   L.d_low = take(T * r * 4);
   L.planes_d = take(3 * T * r * 2);
@@ -140,10 +145,11 @@ moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, con
   if ((r = group(s, ids, L, ws, st)) != MOE_OK) return r;
   if ((r = launch_adapter_low(false, s.T, s.d_in, s.rank, s.n_adapters, x, a, ids,
                               (const int32_t*)(ws + L.offsets), (const int32_t*)(ws + L.rows),
-                              scale, low, nullptr, nullptr, nullptr, nullptr, 0, st)) != MOE_OK)
+                              scale, low, nullptr, nullptr, nullptr, ws + L.terms,
+                              (AdapterTile*)(ws + L.tiles), nullptr, 0, st)) != MOE_OK)
     return r;
-  return launch_adapter_gemm(false, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w, ids, low, b,
-                             y, st);
+  return launch_adapter_gemm(false, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w,
+                             (const AdapterTile*)(ws + L.tiles), ws + L.terms, b, y, st);
 }
 
 moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, const void* x,
@@ -160,12 +166,14 @@ moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, 
   if ((r = group(s, ids, L, ws, st)) != MOE_OK) return r;
   if ((r = launch_adapter_low(
            true, s.T, s.d_out, s.rank, s.n_adapters, d_y, b, ids, offsets, rows, scale, d_low,
-           ws + L.planes_d, low, ws + L.planes_l, arrived,
+           ws + L.planes_d, low, ws + L.planes_l, ws + L.terms, (AdapterTile*)(ws + L.tiles),
+           arrived,
            (int)adapter_outer_arrived_words(s.d_in, s.d_out, s.n_adapters), st)) != MOE_OK)
     return r;
   if (d_x != nullptr &&
-      (r = launch_adapter_gemm(true, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, d_y, w, ids,
-                               d_low, a, d_x, st)) != MOE_OK)
+      (r = launch_adapter_gemm(true, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, d_y, w,
+                               (const AdapterTile*)(ws + L.tiles), ws + L.terms, a, d_x, st)) !=
+          MOE_OK)
     return r;
   return launch_adapter_outer(s.T, s.d_in, s.d_out, s.rank, s.n_adapters, x, d_y,
                               ws + L.planes_d, ws + L.planes_l, offsets, rows, d_a, d_b,

@@ -1,4 +1,4 @@
-// Shared pieces of the adapter kernels: the shape, warp-level matrix instructions on 16 x 8
+// Shared pieces of the adapter kernels: the table of adapters by row tile, warp-level matrix instructions on 16 x 8
 // tiles (used where a product is too thin for the tensor-core pipeline through TMEM) and the
 // split of an fp32 value into bf16 terms.
 #pragma once
@@ -6,6 +6,16 @@
 #include "tc_ptx.cuh"
 
 namespace moe {
+
+// The adapters that have rows in a 256-row tile of the large product, and for each the rows
+// (bit r % 32 of word r / 32) that are NOT its own.
+constexpr int kAdapterTileRows = 256;
+struct AdapterTile {
+  int n;
+  int pad[3];
+  int id[kAdapterTileRows];
+  uint32_t off[kAdapterTileRows][8];
+};
 
 // D[16 x 8] += A[16 x 16] B[16 x 8], bf16 operands, fp32 sums.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,

@@ -7,13 +7,13 @@
 // accumulators double-buffered in TMEM); W is read as it lies, MN-major forward and K-major
 // backward. Bound by the tensor pipe.
 //
-// The adapter term is added in the epilogue, while the next tile's product runs, so it costs no
-// pass over y and no extra k-blocks of the large product: the accumulator is read from TMEM in
-// the layout of the warp-level MMA's accumulators (16x256b), the rank-r product of the warp's
-// 32 rows and 32 columns is made with that MMA, and added. Rows of one warp may belong to
-// several adapters: each one's product is made in registers of its own and selected by row,
-// never multiplied by zero, so an infinity or NaN in one adapter stays in its own rows. low is
-// fp32: it enters as two bf16 terms (error 2^-17), far inside the rounding of the output.
+// The adapter term is a few more k-blocks of the same accumulation: after a tile's product, for
+// each adapter that has rows in the tile, low (A operand) times the adapter's matrix (B operand),
+// with the MMA's lane mask (disable-output-lane) keeping it out of the other rows. Rows of one
+// tile may so belong to any adapters in any order, nothing is multiplied by zero (an infinity
+// or NaN in one adapter stays in its own rows), and the epilogue only stores. low is fp32: it
+// enters as two bf16 terms (error 2^-17), far inside the rounding of the output. The adapters of
+// each 256-row tile and their masks come from a table built with low.
 #include "adapter.cuh"
 #include "ffn_args.cuh"
 
@@ -30,21 +30,29 @@ constexpr int B_HALF = 2 * B_CHUNK;
 constexpr int STAGE_BYTES = A_BYTES + B_HALF;  // 32 KB a CTA
 constexpr int THREADS = 192;                   // producer, MMA, 4 epilogue warps
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int EPI_ROW = 80;  // 32 bf16 of a row, padded: rows hit distinct banks
-constexpr int EPI_WARP = 32 * EPI_ROW;
 constexpr int SMEM_TAIL = 512;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SMEM_TAIL + 4 * EPI_WARP;
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SMEM_TAIL;
 constexpr int GROUP_M = 8;  // row tiles that share the W panels of a wave through L2
 
 struct AdapterGemmArgs {
-  int T, n_out, kblocks, mt, nt, n_adapters, rank;
-  const int32_t* ids;  // [T]
-  const float* low;    // [T, rank]
-  const bf16* w2;      // B [L, rank, n_out] forward, A [L, n_out, rank] backward
-  bf16* out;           // [T, n_out]
+  int T, n_out, kblocks, mt, nt, rank;
+  const AdapterTile* tiles;  // [mt]
+  bf16* out;                 // [T, n_out]
   unsigned* status;
   unsigned long long limit_ns;
 };
+
+// D += A B in the rows whose bit in `off` is clear (rows 32 i ... of the pair in off[i]).
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, const uint32_t (&off)[8]) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, %3, %3;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, "
+      "p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]),
+      "r"(off[4]), "r"(off[5]), "r"(off[6]), "r"(off[7])
+      : "memory");
+}
 
 // Tile w: GROUP_M row tiles at a time, all column tiles of the group.
 __device__ __forceinline__ void tile_of(int w, int mt, int nt, int& m, int& n) {
@@ -54,36 +62,12 @@ __device__ __forceinline__ void tile_of(int w, int mt, int nt, int& m, int& n) {
   n = r / gm;
 }
 
-// Two 16 x 32 halves (TMEM lanes +0 and +16) in the accumulator layout of mma16816: half h,
-// 8-column block i: v[h][i][0..1] at row lane / 4, columns 2 (lane % 4) + 0..1; [2..3] 8 rows on.
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&v)[4][4]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[i][j] = __uint_as_float(r[4 * i + j]);
-}
-
-// Element pair (k, k + 1) of column `col` of the adapter's second matrix as packed bf16.
-template <bool BWD>
-__device__ __forceinline__ uint32_t w2_pair(const bf16* w2, int n_out, int rank, int k, int col) {
-  if (BWD) return *reinterpret_cast<const uint32_t*>(w2 + (size_t)col * rank + k);
-  const uint16_t* p = reinterpret_cast<const uint16_t*>(w2) + (size_t)k * n_out + col;
-  return (uint32_t)p[0] | ((uint32_t)p[n_out] << 16);
-}
-
 template <bool BWD>
 __global__ void __launch_bounds__(THREADS, 1)
     adapter_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
-                        const __grid_constant__ CUtensorMap tmB, const AdapterGemmArgs g) {
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmLow,
+                        const __grid_constant__ CUtensorMap tmM, const AdapterGemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t* full = (uint64_t*)(base + STAGES * STAGE_BYTES);  // leader: both CTAs' bytes landed
@@ -93,7 +77,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = (uint32_t*)(done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-  uint8_t* epi = base + STAGES * STAGE_BYTES + SMEM_TAIL;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
@@ -101,6 +84,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int pair = (int)cluster_id_x(), npairs = (int)num_clusters_x();
   const int total = g.mt * g.nt;
   const uint64_t limit = g.limit_ns;
+  // Ring stages after a tile's k-blocks: for each group of its adapters, low (nl stages, both
+  // terms) and then nl stages an adapter; low's stages are freed with the group, so a group and
+  // its low fit the ring together.
+  const int nl = (g.rank + 63) / 64, group = nl == 1 ? 4 : 2;
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -130,18 +117,33 @@ __global__ void __launch_bounds__(THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_par = 0;
       bool ok = true;
+      // the next stage, when it is free: its full barrier (the leader's) expecting `bytes` a CTA
+      auto begin = [&](uint32_t bytes, uint32_t& fb, uint32_t& a) {
+        if (!mbar_wait<true>(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) {
+          ok = false;
+          return false;
+        }
+        fb = map_rank(saddr(&full[stage]), 0);
+        a = saddr(base + stage * STAGE_BYTES);
+        if (leader) mbar_expect_tx(saddr(&full[stage]), 2 * bytes);
+        issued_mask |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return true;
+      };
       for (int w = pair; w < total && ok; w += npairs) {
         int m, n;
         tile_of(w, g.mt, g.nt, m, n);
         const int m0 = m * PAIR_M + (int)rank * BM, n0 = n * BN + (int)rank * 128;
+        const AdapterTile* at = g.tiles + m;
+        const int n_ad = at->n;
+        uint32_t fb, a;
         for (int kb = 0; kb < g.kblocks; ++kb) {
-          if (!mbar_wait<true>(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = map_rank(saddr(&full[stage]), 0);  // the leader's barrier
-          if (leader) mbar_expect_tx(saddr(&full[stage]), 2 * STAGE_BYTES);
-          const uint32_t a = saddr(base + stage * STAGE_BYTES), b = a + A_BYTES;
+          if (!begin(STAGE_BYTES, fb, a)) break;
+          const uint32_t b = a + A_BYTES;
           tma_load_2d_pair(a, &tmA, kb * BK, m0, fb);
           if (BWD) {
             tma_load_2d_pair(b, &tmB, kb * BK, n0, fb);
@@ -149,11 +151,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             tma_load_2d_pair(b, &tmB, n0, kb * BK, fb);
             tma_load_2d_pair(b + B_CHUNK, &tmB, n0 + 64, kb * BK, fb);
           }
-          issued_mask |= 1u << stage;
-          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+        }
+        for (int i = 0; i < n_ad && ok; ++i) {
+          if (i % group == 0)
+            for (int j = 0; j < nl; ++j) {
+              if (!begin(STAGE_BYTES, fb, a)) break;
+              tma_load_3d_pair(a, &tmLow, 64 * j, m0, 0, fb);
+              tma_load_3d_pair(a + A_BYTES, &tmLow, 64 * j, m0, 1, fb);
+            }
+          const int l = at->id[i];
+          for (int j = 0; j < nl && ok; ++j) {
+            if (!begin(B_HALF, fb, a)) break;
+            const uint32_t b = a + A_BYTES;
+            if (BWD) {
+              tma_load_3d_pair(b, &tmM, 64 * j, n0, l, fb);
+            } else {
+              tma_load_3d_pair(b, &tmM, n0, 64 * j, l, fb);
+              tma_load_3d_pair(b + B_CHUNK, &tmM, n0 + 64, 64 * j, l, fb);
+            }
           }
         }
       }
@@ -175,7 +190,29 @@ __global__ void __launch_bounds__(THREADS, 1)
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
+      // the next stage's index, once both CTAs' halves have landed; -1 when the wait ran out
+      auto next = [&]() {
+        if (!mbar_wait<true>(saddr(&full[stage]), phase, abort_flag, g.status, limit)) {
+          ok = false;
+          return -1;
+        }
+        tc_fence_after();
+        const int s = stage;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return s;
+      };
+      auto release = [&](int s) {
+        tc_commit<2>(saddr(&empty[s]));
+        tc_commit<2>(map_rank(saddr(&empty[s]), 1));
+      };
       for (int w = pair; w < total && ok; w += npairs, ++it) {
+        int m, n;
+        tile_of(w, g.mt, g.nt, m, n);
+        const AdapterTile* at = g.tiles + m;
+        const int n_ad = at->n;
         const int buf = it & 1;
         const uint32_t use = (uint32_t)(it >> 1);
         if (!mbar_wait<true>(saddr(&tempty[buf]), (use & 1u) ^ 1u, abort_flag, g.status, limit))
@@ -183,24 +220,44 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(buf * BN);
         for (int kb = 0; kb < g.kblocks; ++kb) {
-          if (!mbar_wait<true>(saddr(&full[stage]), phase, abort_flag, g.status, limit)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a = saddr(base + stage * STAGE_BYTES), b = a + A_BYTES;
+          const int s = next();
+          if (s < 0) break;
+          const uint32_t a = saddr(base + s * STAGE_BYTES), b = a + A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
             tc_mma<2>(d, desc_sw128(a + kk * 32, 16, 1024),
                       BWD ? desc_sw128(b + kk * 32, 16, 1024)
                           : desc_sw128(b + kk * 2048, B_CHUNK, 1024),
                       idesc, (kb | kk) != 0 ? 1u : 0u);
-          tc_commit<2>(saddr(&empty[stage]));
-          tc_commit<2>(map_rank(saddr(&empty[stage]), 1));
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+          release(s);
+        }
+        int low[2] = {0, 0};
+        for (int i = 0; i < n_ad && ok; ++i) {
+          uint32_t off[8];
+          {
+            const uint4* mp = reinterpret_cast<const uint4*>(at->off[i]);
+            const uint4 u = mp[0], v = mp[1];
+            off[0] = u.x; off[1] = u.y; off[2] = u.z; off[3] = u.w;
+            off[4] = v.x; off[5] = v.y; off[6] = v.z; off[7] = v.w;
           }
+          if (i % group == 0)
+            for (int j = 0; j < nl && ok; ++j) low[j] = next();
+          for (int j = 0; j < nl && ok; ++j) {
+            const int s = next();
+            if (s < 0) break;
+            const uint32_t a = saddr(base + low[j] * STAGE_BYTES);
+            const uint32_t b = saddr(base + s * STAGE_BYTES) + A_BYTES;
+            const int steps = min(4, (g.rank - 64 * j + 15) / 16);
+            for (int kk = 0; kk < steps; ++kk) {
+              const uint64_t bd = BWD ? desc_sw128(b + kk * 32, 16, 1024)
+                                      : desc_sw128(b + kk * 2048, B_CHUNK, 1024);
+              mma_rows(d, desc_sw128(a + kk * 32, 16, 1024), bd, idesc, off);
+              mma_rows(d, desc_sw128(a + A_BYTES + kk * 32, 16, 1024), bd, idesc, off);
+            }
+            release(s);
+          }
+          if (ok && (i % group == group - 1 || i == n_ad - 1))
+            for (int j = 0; j < nl; ++j) release(low[j]);
         }
         if (ok) {
           tc_commit<2>(saddr(&tfull[buf]));
@@ -216,26 +273,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;  // TMEM lanes 32 q ...
     const uint32_t tempty_leader = map_rank(saddr(&tempty[0]), 0);
-    uint8_t* ebuf = epi + q * EPI_WARP;
-    const int lr = lane >> 2, lc = lane & 3;
     int it = 0;
     for (int w = pair; w < total; w += npairs, ++it) {
       int m, n;
       tile_of(w, g.mt, g.nt, m, n);
       const int buf = it & 1;
       const uint32_t use = (uint32_t)(it >> 1);
-      const int row0 = m * PAIR_M + (int)rank * BM + q * 32;
-      // this lane's four rows (lr + 8 i) and their adapters
-      int id[4];
-      const float* lrow[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = row0 + lr + 8 * i;
-        int l = r < g.T ? g.ids[r] : -1;
-        if (l < 0 || l >= g.n_adapters) l = -1;  // the grouping kernel has reported bad ids
-        id[i] = l;
-        lrow[i] = g.low + (size_t)min(r, g.T - 1) * g.rank;
-      }
       int w_ok = 0;
       if (lane == 0)
         w_ok = mbar_wait<true>(saddr(&tfull[buf]), use & 1u, abort_flag, g.status, limit);
@@ -243,85 +286,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!w_ok) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + (uint32_t)(buf * BN) + ((uint32_t)(q * 32) << 16);
+      const int r = m * PAIR_M + (int)rank * BM + q * 32 + lane;
+      bf16* orow = g.out + (size_t)min(r, g.T - 1) * g.n_out;
 #pragma unroll 1
       for (int c = 0; c < BN / 32; ++c) {
-        const int col0 = n * BN + c * 32;
-        if (col0 >= g.n_out) break;  // warp-uniform (n_out is a multiple of 64)
-        float acc[2][4][4];
-        tmem_ld_16x256(tb + c * 32, acc[0]);
-        tmem_ld_16x256(tb + c * 32 + (16u << 16), acc[1]);
-        int last = -1;
-        while (true) {  // the warp's adapters, in ascending order
-          int nx = 0x7fffffff;
+        const int col = n * BN + c * 32;
+        if (col >= g.n_out) break;  // warp-uniform (n_out is a multiple of 64)
+        uint32_t v[32];
+        tmem_ld32(tb + c * 32, v);
+        tmem_ld_wait();
+        if (r < g.T) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + col);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (id[i] > last) nx = min(nx, id[i]);
-          nx = __reduce_min_sync(0xffffffffu, nx);
-          if (nx == 0x7fffffff) break;
-          last = nx;
-          const bf16* w2 = g.w2 + (size_t)nx * g.rank * g.n_out;
-          float dl[2][4][4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) dl[h][i][j] = 0.f;
-          for (int k0 = 0; k0 < g.rank; k0 += 16) {
-            const bool second = k0 + 8 < g.rank;  // rank is a multiple of 8
-            uint32_t b0[4], b1[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int col = col0 + 8 * i + lr;
-              b0[i] = w2_pair<BWD>(w2, g.n_out, g.rank, k0 + 2 * lc, col);
-              b1[i] = second ? w2_pair<BWD>(w2, g.n_out, g.rank, k0 + 8 + 2 * lc, col) : 0u;
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int p = 0; p < 4; ++p) {  // (rows lr, lr + 8) x (k, k + 8)
-                float2 f = make_float2(0.f, 0.f);
-                if (p < 2 || second)
-                  f = *reinterpret_cast<const float2*>(lrow[2 * h + (p & 1)] + k0 + 8 * (p >> 1) +
-                                                       2 * lc);
-                hi[p] = take_bf16x2(f.x, f.y);
-                lo[p] = pack_bf16x2(f.x, f.y);
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                mma16816(dl[h][i], hi, b0[i], b1[i]);
-                mma16816(dl[h][i], lo, b0[i], b1[i]);
-              }
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (id[2 * h + (j >> 1)] == nx) acc[h][i][j] += dl[h][i][j];
+          for (int j = 0; j < 4; ++j)
+            dst[j] = make_uint4(
+                pack_bf16x2(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1])),
+                pack_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3])),
+                pack_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5])),
+                pack_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7])));
         }
-        // through the warp's buffer: 16-byte stores of whole 64-byte row pieces
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              *reinterpret_cast<uint32_t*>(ebuf + (16 * h + 8 * j + lr) * EPI_ROW + i * 16 +
-                                           lc * 4) =
-                  pack_bf16x2(acc[h][i][2 * j], acc[h][i][2 * j + 1]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = row0 + lr + 8 * i;
-          if (r < g.T)
-            *reinterpret_cast<uint4*>(g.out + (size_t)r * g.n_out + col0 + lc * 8) =
-                *reinterpret_cast<const uint4*>(ebuf + (lr + 8 * i) * EPI_ROW + lc * 16);
-        }
-        __syncwarp();  // the buffer is free for the next columns
       }
       tc_fence_before();
       __syncwarp();
@@ -338,8 +321,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <bool BWD>
-moe_status run(const CUtensorMap& ma, const CUtensorMap& mb, const AdapterGemmArgs& a,
-               cudaStream_t st) {
+moe_status run(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& ml,
+               const CUtensorMap& mm, const AdapterGemmArgs& a, cudaStream_t st) {
   auto kern = adapter_gemm_kernel<BWD>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) !=
       cudaSuccess)
@@ -348,17 +331,17 @@ moe_status run(const CUtensorMap& ma, const CUtensorMap& mb, const AdapterGemmAr
   if (pairs > a.mt * a.nt) pairs = a.mt * a.nt;
   launch_begin(K_ADAPTER_GEMM, st);
   launch_kernel(kern, dim3((unsigned)(2 * pairs)), dim3(THREADS), (size_t)SMEM_BYTES, st, 2, ma,
-                mb, a);
+                mb, ml, mm, a);
   return launch_end(K_ADAPTER_GEMM, st);
 }
 
 }  // namespace
 
-// in [T, k_dim], w [d_in, d_out]; forward: k_dim = d_in, out [T, d_out], w2 = B; backward:
-// k_dim = d_out, out [T, d_in], w2 = A.
+// in [T, k_dim], w [d_in, d_out]; forward: k_dim = d_in, out [T, d_out], m = B; backward:
+// k_dim = d_out, out [T, d_in], m = A. low: [2][T][rank] bf16 terms.
 moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
-                               const void* in, const void* w, const int32_t* ids,
-                               const float* low, const void* w2, void* out, cudaStream_t st) {
+                               const void* in, const void* w, const AdapterTile* tiles,
+                               const void* low, const void* m, void* out, cudaStream_t st) {
   AdapterGemmArgs a = {};
   const int k_dim = bwd ? d_out : d_in, n_out = bwd ? d_in : d_out;
   a.T = T;
@@ -366,22 +349,25 @@ moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapt
   a.kblocks = k_dim / BK;
   a.mt = (T + PAIR_M - 1) / PAIR_M;
   a.nt = (n_out + BN - 1) / BN;
-  a.n_adapters = n_adapters;
   a.rank = rank;
-  a.ids = ids;
-  a.low = low;
-  a.w2 = (const bf16*)w2;
+  a.tiles = tiles;
   a.out = (bf16*)out;
   a.status = device_status_ptr();
   a.limit_ns = kWaitLimitNs;
-  CUtensorMap ma, mb;
-  const uint64_t ad[2] = {(uint64_t)k_dim, (uint64_t)T}, as[1] = {(uint64_t)k_dim * 2};
+  CUtensorMap ma, mb, ml, mm;
+  const uint64_t r = rank, t = T, n = n_out, L = n_adapters;
+  const uint64_t ad[2] = {(uint64_t)k_dim, t}, as[1] = {(uint64_t)k_dim * 2};
   const uint32_t abox[2] = {64, 128};
   const uint64_t bd[2] = {(uint64_t)d_out, (uint64_t)d_in}, bs[1] = {(uint64_t)d_out * 2};
   const uint32_t bbox[2] = {64, bwd ? 128u : 64u};
-  if (!make_map(&ma, in, 2, ad, as, abox) || !make_map(&mb, w, 2, bd, bs, bbox))
+  const uint64_t ld[3] = {r, t, 2}, ls[2] = {r * 2, t * r * 2};
+  const uint32_t lbox[3] = {64, 128, 1};
+  const uint64_t md[3] = {bwd ? r : n, bwd ? n : r, L}, ms[2] = {(bwd ? r : n) * 2, r * n * 2};
+  const uint32_t mbox[3] = {64, bwd ? 128u : 64u, 1};
+  if (!make_map(&ma, in, 2, ad, as, abox) || !make_map(&mb, w, 2, bd, bs, bbox) ||
+      !make_map(&ml, low, 3, ld, ls, lbox) || !make_map(&mm, m, 3, md, ms, mbox))
     return MOE_ERR_CUDA;
-  return bwd ? run<true>(ma, mb, a, st) : run<false>(ma, mb, a, st);
+  return bwd ? run<true>(ma, mb, ml, mm, a, st) : run<false>(ma, mb, ml, mm, a, st);
 }
 
 }  // namespace moe

@@ -23,7 +23,6 @@ constexpr int ROWS = 64;   // rows of a grouped tile: 16 a warp
 constexpr int KC = 64;     // contraction per stage
 constexpr int STAGES = 4;
 constexpr int SPLIT = 4;   // CTAs of a cluster that split the contraction
-constexpr int MAXL = 256;
 
 // ------------------------------------------------------------------ grouped
 struct LowArgs {
@@ -37,10 +36,21 @@ struct LowArgs {
   bf16* planes;    // NULL, or low in slot order as three bf16 terms: [3][T][r]
   const float* low2;  // with planes: another [T, r] ...
   bf16* planes2;      // ... put into slot order the same way
+  bf16* terms;        // [2][T][r]: low as two bf16 terms
+  AdapterTile* tiles; // [ceil(T / 256)]
+  int tile_clusters;  // clusters up to here make low, those behind the table of tiles
   uint32_t* clear;    // words to zero for the kernel that follows (or none)
   int n_clear;
   int T, D, r, L;
 };
+
+// Where the 16-byte piece c of row r lies in a tile of NT pieces a row, so that the eight rows
+// that one ldmatrix phase reads fall on distinct banks.
+template <int NT>
+__device__ __forceinline__ uint32_t piece(int r, int c) {
+  const int x = NT >= 8 ? r & 7 : NT == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
+  return (uint32_t)(r * (NT * 16) + ((c ^ x) << 4));
+}
 
 // Adapter l and first slot of row tile `tile` (ROWS rows); l = -1 past the last tile.
 __device__ __forceinline__ void find_tile(const int32_t* offsets, int L, int tile, int rows,
@@ -66,6 +76,39 @@ __device__ __forceinline__ void find_tile(const int32_t* offsets, int L, int til
   }
 }
 
+// Entry `m` of the table of tiles: which adapters have rows in 256 m ..., and which rows.
+__device__ __forceinline__ void make_tile(int m, const LowArgs& g, uint8_t* smem) {
+  const int r0 = m * kAdapterTileRows, tid = threadIdx.x, lane = tid & 31;
+  if (r0 >= g.T) return;
+  uint32_t* own = reinterpret_cast<uint32_t*>(smem);  // [L][8]
+  for (int i = tid; i < g.L * 8; i += THREADS) own[i] = 0u;
+  __syncthreads();
+  for (int r = tid; r < kAdapterTileRows && r0 + r < g.T; r += THREADS) {
+    const int l = g.ids[r0 + r];
+    if (l >= 0 && l < g.L) atomicOr(&own[l * 8 + (r >> 5)], 1u << (r & 31));
+  }
+  __syncthreads();
+  if (tid >= 32) return;
+  AdapterTile* t = g.tiles + m;
+  int n = 0;
+  for (int l0 = 0; l0 < g.L; l0 += 32) {
+    const int l = l0 + lane;
+    uint32_t any = 0;
+    if (l < g.L)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) any |= own[l * 8 + i];
+    const unsigned has = __ballot_sync(0xffffffffu, any != 0u);
+    if (any != 0u) {
+      const int at = n + __popc(has & lanemask_lt());
+      t->id[at] = l;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t->off[at][i] = ~own[l * 8 + i];
+    }
+    n += __popc(has);
+  }
+  if (lane == 0) t->n = n;
+}
+
 // NT: 8-column blocks of the rank, rounded up to 2, 4, 8 or 16.
 template <bool TRANS, int NT>
 __global__ void __launch_bounds__(THREADS) adapter_low_kernel(const LowArgs g) {
@@ -77,6 +120,10 @@ __global__ void __launch_bounds__(THREADS) adapter_low_kernel(const LowArgs g) {
   pdl_wait();  // the previous kernel in the stream has completed
   pdl_trigger();
   for (int i = blockIdx.x * THREADS + tid; i < g.n_clear; i += gridDim.x * THREADS) g.clear[i] = 0u;
+  if ((int)cluster_id_x() >= g.tile_clusters) {
+    make_tile(((int)cluster_id_x() - g.tile_clusters) * SPLIT + rank, g, smem);
+    return;  // the whole cluster
+  }
   // rows without an adapter
   for (int t = blockIdx.x * THREADS + tid; t < g.T; t += gridDim.x * THREADS) {
     const int l = g.ids[t];
@@ -125,7 +172,7 @@ __global__ void __launch_bounds__(THREADS) adapter_low_kernel(const LowArgs g) {
       for (int i = tid; i < KC * NT; i += THREADS) {
         const int k = i / NT, c = i % NT;
         const bool real = c * 8 < g.r;
-        cp_async16_if(ms + k * (NT * 16) + c * 16,
+        cp_async16_if(ms + piece<NT>(k, c),
                       ml + (size_t)(kb * KC + k) * g.r + (real ? c * 8 : 0), real);
       }
     }
@@ -161,7 +208,7 @@ __global__ void __launch_bounds__(THREADS) adapter_low_kernel(const LowArgs g) {
           ldmatrix4(b, ms + j * 128 + ((c ^ (j & 7)) << 4));
         } else {
           const int k = kk * 16 + (lane & 15), c = i + (lane >> 4);
-          ldmatrix4t(b, ms + k * (NT * 16) + c * 16);
+          ldmatrix4t(b, ms + piece<NT>(k, c));
         }
         mma16816(acc[i], a, b[0], b[1]);
         mma16816(acc[i + 1], a, b[2], b[3]);
@@ -200,6 +247,11 @@ __global__ void __launch_bounds__(THREADS) adapter_low_kernel(const LowArgs g) {
     v1 *= sc;
     const size_t o = (size_t)s_row[r] * g.r + j;
     *reinterpret_cast<float2*>(g.low + o) = make_float2(v0, v1);
+    {
+      float a0 = v0, a1 = v1;
+      *reinterpret_cast<uint32_t*>(g.terms + o) = take_bf16x2(a0, a1);
+      *reinterpret_cast<uint32_t*>(g.terms + (size_t)g.T * g.r + o) = pack_bf16x2(a0, a1);
+    }
     if (g.planes != nullptr) {
       const size_t slot = (size_t)(first + r) * g.r + j, plane = (size_t)g.T * g.r;
       float2 w = *reinterpret_cast<const float2*>(g.low2 + o);
@@ -215,15 +267,17 @@ __global__ void __launch_bounds__(THREADS) adapter_low_kernel(const LowArgs g) {
 }
 
 template <bool TRANS, int NT>
-moe_status run_low(const LowArgs& a, cudaStream_t st) {
+moe_status run_low(LowArgs a, cudaStream_t st) {
   auto kern = adapter_low_kernel<TRANS, NT>;
   const int smem = STAGES * (ROWS * KC * 2 + KC * NT * 16);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MOE_ERR_CUDA;
   // at most T / ROWS whole tiles and one ragged tile an adapter (or a row)
   const int ragged = a.L < a.T ? a.L : a.T;
+  a.tile_clusters = a.T / ROWS + ragged;
+  const int table = (a.T + SPLIT * kAdapterTileRows - 1) / (SPLIT * kAdapterTileRows);
   launch_begin(K_ADAPTER_LOW, st);
-  launch_kernel(kern, dim3((unsigned)(SPLIT * (a.T / ROWS + ragged))), dim3(THREADS),
+  launch_kernel(kern, dim3((unsigned)(SPLIT * (a.tile_clusters + table))), dim3(THREADS),
                 (size_t)smem, st, SPLIT, a);
   return launch_end(K_ADAPTER_LOW, st);
 }
@@ -384,7 +438,7 @@ __global__ void __launch_bounds__(THREADS) adapter_outer_kernel(const OuterArgs 
     for (int i = tid; i < 3 * OT * NT; i += THREADS) {
       const int q = i / (OT * NT), r = i / NT % OT, c = i % NT;
       const bool on = r0 + r < n && c * 8 < g.r;
-      cp_async16_if(ps + q * P_BYTES + r * (NT * 16) + c * 16,
+      cp_async16_if(ps + q * P_BYTES + piece<NT>(r, c),
                     planes + q * plane + (on ? (size_t)(lo + r0 + r) * g.r + c * 8 : 0), on);
     }
   };
@@ -421,8 +475,7 @@ __global__ void __launch_bounds__(THREADS) adapter_outer_kernel(const OuterArgs 
 #pragma unroll
         for (int i = 0; i < NT; i += 2) {
           uint32_t b[4];
-          ldmatrix4t(b, ps + q * P_BYTES + (kk * 16 + (lane & 15)) * (NT * 16) +
-                            (i + (lane >> 4)) * 16);
+          ldmatrix4t(b, ps + q * P_BYTES + piece<NT>(kk * 16 + (lane & 15), i + (lane >> 4)));
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             mma16816(acc[m][i], a[m], b[0], b[1]);
@@ -513,10 +566,12 @@ size_t adapter_outer_arrived_words(int d_in, int d_out, int L) {
 moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void* in,
                               const void* m, const int32_t* ids, const int32_t* offsets,
                               const int32_t* rows, const float* scale, float* low, void* planes,
-                              const float* low2, void* planes2, uint32_t* clear,
-                              int n_clear, cudaStream_t st) {
-  const LowArgs a{(const bf16*)in, (const bf16*)m, ids,     offsets, rows, scale, low,
-                  (bf16*)planes,   low2,           (bf16*)planes2,  clear, n_clear, T, D, r, L};
+                              const float* low2, void* planes2, void* terms,
+                              AdapterTile* tiles, uint32_t* clear, int n_clear,
+                              cudaStream_t st) {
+  const LowArgs a{(const bf16*)in, (const bf16*)m,  ids,          offsets, rows, scale, low,
+                  (bf16*)planes,   low2,            (bf16*)planes2, (bf16*)terms, tiles, 0,
+                  clear,           n_clear,         T,            D,       r,    L};
   return trans ? run_low_nt<true>(a, st) : run_low_nt<false>(a, st);
 }
 
