@@ -28,18 +28,16 @@ moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void
                               const void* m, const int32_t* ids, const int32_t* offsets,
                               const int32_t* rows, const float* scale, float* low, void* planes,
                               const float* low2, void* planes2, void* terms,
-                              AdapterTile* tiles, uint32_t* clear, int n_clear,
-                              cudaStream_t st);
+                              AdapterTile* tiles, cudaStream_t st);
 moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
                                const void* in, const void* w, const AdapterTile* tiles,
                                const void* low, const void* m, void* out, cudaStream_t st);
 size_t adapter_outer_part_bytes(int T, int d_in, int d_out, int r);
-size_t adapter_outer_arrived_words(int d_in, int d_out, int L);
 moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
                                 const void* d_y, const void* planes_d_low,
                                 const void* planes_low, const int32_t* offsets,
                                 const int32_t* rows, float* d_a, float* d_b, float* part,
-                                uint32_t* arrived, cudaStream_t st);
+                                cudaStream_t st);
 
 namespace {
 
@@ -83,7 +81,7 @@ FewLayout few_layout(const moe_adapter_shape& s) {
 struct Layout {
   size_t counts, offsets, a2p, rows, scratch;                    // grouping
   size_t tiles, terms;                                           // for the large product
-  size_t d_low, planes_d, planes_l, arrived, part, total_fwd, total;  // backward
+  size_t d_low, planes_d, planes_l, part, total_fwd, total;  // backward
 };
 Layout layout(const moe_adapter_shape& s) {
   Layout L;
@@ -105,7 +103,6 @@ Layout layout(const moe_adapter_shape& s) {
   L.d_low = take(T * r * 4);
   L.planes_d = take(3 * T * r * 2);
   L.planes_l = take(3 * T * r * 2);
-  L.arrived = take(adapter_outer_arrived_words(s.d_in, s.d_out, s.n_adapters) * 4);
   L.part = take(adapter_outer_part_bytes(s.T, s.d_in, s.d_out, s.rank));
   L.total = o;
   return L;
@@ -146,7 +143,7 @@ moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, con
   if ((r = launch_adapter_low(false, s.T, s.d_in, s.rank, s.n_adapters, x, a, ids,
                               (const int32_t*)(ws + L.offsets), (const int32_t*)(ws + L.rows),
                               scale, low, nullptr, nullptr, nullptr, ws + L.terms,
-                              (AdapterTile*)(ws + L.tiles), nullptr, 0, st)) != MOE_OK)
+                              (AdapterTile*)(ws + L.tiles), st)) != MOE_OK)
     return r;
   return launch_adapter_gemm(false, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w,
                              (const AdapterTile*)(ws + L.tiles), ws + L.terms, b, y, st);
@@ -161,14 +158,12 @@ moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, 
   const int32_t* offsets = (const int32_t*)(ws + L.offsets);
   const int32_t* rows = (const int32_t*)(ws + L.rows);
   float* d_low = (float*)(ws + L.d_low);
-  uint32_t* arrived = (uint32_t*)(ws + L.arrived);
   moe_status r;
   if ((r = group(s, ids, L, ws, st)) != MOE_OK) return r;
   if ((r = launch_adapter_low(
            true, s.T, s.d_out, s.rank, s.n_adapters, d_y, b, ids, offsets, rows, scale, d_low,
            ws + L.planes_d, low, ws + L.planes_l, ws + L.terms, (AdapterTile*)(ws + L.tiles),
-           arrived,
-           (int)adapter_outer_arrived_words(s.d_in, s.d_out, s.n_adapters), st)) != MOE_OK)
+           st)) != MOE_OK)
     return r;
   if (d_x != nullptr &&
       (r = launch_adapter_gemm(true, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, d_y, w,
@@ -177,7 +172,7 @@ moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, 
     return r;
   return launch_adapter_outer(s.T, s.d_in, s.d_out, s.rank, s.n_adapters, x, d_y,
                               ws + L.planes_d, ws + L.planes_l, offsets, rows, d_a, d_b,
-                              (float*)(ws + L.part), arrived, st);
+                              (float*)(ws + L.part), st);
 }
 
 }  // namespace moe

@@ -4,13 +4,16 @@
 //             (forward: in = x, M = A_l [d_in, r]; backward: in = d_y, M = B_l^T, B_l [r, d_out])
 //   few:      partial sums of x[t] A_l for at most 128 rows, and the control words of the
 //             kernel that follows
-//   outer:    dA_l = sum_t x[t]^T d_low[t],  dB_l = sum_t low[t]^T d_y[t], t over l's rows
 //
-// All are bound by reading the wide rows (r is 8 ... 128, the rows are thousands wide), so they
-// use the warp-level MMA (16 x 8 tiles fit the rank) fed by cp.async. Rows are grouped by
-// adapter with the layer's stable permutation, so a tile never mixes adapters.
+// Bound by reading the wide rows once. The grouped form gives a cluster of four CTAs up to 128
+// rows of one adapter (grouping is the layer's stable permutation, so a tile never mixes
+// adapters) and splits the contraction over them: enough bytes in flight from few rows. Rows
+// are gathered by cp.async, the adapter's matrix comes by TMA as it lies, the product runs on
+// the tensor cores (M = rows, N = rank), and the four partials are added in rank order through
+// distributed shared memory.
 #include "adapter.cuh"
 #include "few.cuh"
+#include "ffn_args.cuh"
 
 namespace moe {
 
@@ -18,16 +21,17 @@ namespace {
 
 using namespace ptx;
 
-constexpr int THREADS = 128;
-constexpr int ROWS = 64;   // rows of a grouped tile: 16 a warp
+constexpr int ROWS = 128;  // rows of a grouped tile
 constexpr int KC = 64;     // contraction per stage
 constexpr int STAGES = 4;
 constexpr int SPLIT = 4;   // CTAs of a cluster that split the contraction
+constexpr int LOADERS = 128, THREADS = 192;  // four gather / store warps, MMA warp, TMA warp
+constexpr int X_BYTES = ROWS * KC * 2;       // 16 KB
+constexpr int M_CHUNK = 8192;                // 64 x 64 of the adapter's matrix
 
 // ------------------------------------------------------------------ grouped
 struct LowArgs {
   const bf16* in;   // [T, D]
-  const bf16* m;    // [L, D, r], or [L, r, D] (TRANS)
   const int32_t* ids;
   const int32_t* offsets;  // [L + 1]
   const int32_t* rows;     // slot -> row
@@ -39,18 +43,11 @@ struct LowArgs {
   bf16* terms;        // [2][T][r]: low as two bf16 terms
   AdapterTile* tiles; // [ceil(T / 256)]
   int tile_clusters;  // clusters up to here make low, those behind the table of tiles
-  uint32_t* clear;    // words to zero for the kernel that follows (or none)
-  int n_clear;
   int T, D, r, L;
+  int n_mma, nc;      // the rank rounded up to 16; its 64-wide pieces
+  unsigned* status;
+  unsigned long long limit_ns;
 };
-
-// Where the 16-byte piece c of row r lies in a tile of NT pieces a row, so that the eight rows
-// that one ldmatrix phase reads fall on distinct banks.
-template <int NT>
-__device__ __forceinline__ uint32_t piece(int r, int c) {
-  const int x = NT >= 8 ? r & 7 : NT == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
-  return (uint32_t)(r * (NT * 16) + ((c ^ x) << 4));
-}
 
 // Adapter l and first slot of row tile `tile` (ROWS rows); l = -1 past the last tile.
 __device__ __forceinline__ void find_tile(const int32_t* offsets, int L, int tile, int rows,
@@ -109,134 +106,195 @@ __device__ __forceinline__ void make_tile(int m, const LowArgs& g, uint8_t* smem
   if (lane == 0) t->n = n;
 }
 
-// NT: 8-column blocks of the rank, rounded up to 2, 4, 8 or 16.
-template <bool TRANS, int NT>
-__global__ void __launch_bounds__(THREADS) adapter_low_kernel(const LowArgs g) {
-  constexpr int X_BYTES = ROWS * KC * 2, M_BYTES = KC * NT * 8 * 2, ST = X_BYTES + M_BYTES;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_l, s_first, s_row[ROWS];
+// TRANS: the adapter's matrix is [r, D] (the backward's B_l), else [D, r].
+template <bool TRANS>
+__global__ void __launch_bounds__(THREADS)
+    adapter_low_kernel(const __grid_constant__ CUtensorMap tmM, const LowArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[STAGES], empty[STAGES], done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_l, s_first, s_abort, s_row[ROWS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_rank();
+  uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t sb = saddr(base);
+  const int st_bytes = X_BYTES + g.nc * M_CHUNK;
+  volatile int* abort_flag = &s_abort;
+  uint32_t tcols = 32;
+  while ((int)tcols < g.n_mma) tcols *= 2;
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(saddr(&full[s]), LOADERS + 1);
+      mbar_init(saddr(&empty[s]), 1);
+    }
+    mbar_init(saddr(&done), 1);
+    s_abort = 0;
+    s_l = -1;
+    mbar_init_fence();
+  }
+  __syncthreads();
   pdl_wait();  // the previous kernel in the stream has completed
   pdl_trigger();
-  for (int i = blockIdx.x * THREADS + tid; i < g.n_clear; i += gridDim.x * THREADS) g.clear[i] = 0u;
   if ((int)cluster_id_x() >= g.tile_clusters) {
-    make_tile(((int)cluster_id_x() - g.tile_clusters) * SPLIT + rank, g, smem);
+    make_tile(((int)cluster_id_x() - g.tile_clusters) * SPLIT + rank, g, base);
     return;  // the whole cluster
   }
   // rows without an adapter
-  for (int t = blockIdx.x * THREADS + tid; t < g.T; t += gridDim.x * THREADS) {
+  for (int t = blockIdx.x * THREADS + tid; t < g.T; t += SPLIT * g.tile_clusters * THREADS) {
     const int l = g.ids[t];
     if (l < 0 || l >= g.L)
       for (int j = 0; j < g.r; j += 4)
         *reinterpret_cast<float4*>(g.low + (size_t)t * g.r + j) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  if (tid == 0) s_l = -1;
-  __syncthreads();
   if (warp == 0) find_tile(g.offsets, g.L, (int)cluster_id_x(), ROWS, &s_l, &s_first);
   __syncthreads();
   const int l = s_l;
   if (l < 0) return;  // the whole cluster: past the last tile
+  if (warp == 4) tmem_alloc<1>(saddr(&s_tmem), tcols);
   const int first = s_first, n = min(ROWS, g.offsets[l + 1] - first);
   if (tid < ROWS) s_row[tid] = tid < n ? g.rows[first + tid] : -1;
+  tc_fence_before();
   __syncthreads();
-
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
   const int kblocks = g.D / KC;
   const int kb0 = rank * kblocks / SPLIT, kb1 = (rank + 1) * kblocks / SPLIT;
-  const uint32_t sb = saddr(smem);
-  // this thread's pieces of the x tile: rows tid / 8 + 16 i, 16-byte piece tid % 8
-  const int pc = tid & 7, pr = tid >> 3;
-  const bf16* src[4];
-  uint32_t dst[4];
-  bool on[4];
+  const uint64_t limit = g.limit_ns;
+  bool ok = true;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ gather
+    // 16-byte piece tid % 8 of rows tid / 8 + 16 i: a warp copies whole 128-byte lines
+    const int pc = tid & 7, pr = tid >> 3;
+    const bf16* src[8];
+    unsigned on = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = pr + 16 * i, t = s_row[r];
-    on[i] = t >= 0;
-    src[i] = g.in + (size_t)(on[i] ? t : 0) * g.D + pc * 8;
-    dst[i] = (uint32_t)(r * 128 + ((pc ^ (r & 7)) << 4));
-  }
-  const bf16* ml = g.m + (size_t)l * g.D * g.r;
-  auto load = [&](int kb, int stage) {
-    const uint32_t xs = sb + stage * ST, ms = xs + X_BYTES;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) cp_async16_if(xs + dst[i], src[i] + (size_t)kb * KC, on[i]);
-    if (TRANS) {  // [NT * 8 rank rows][KC], swizzled
-      for (int i = tid; i < NT * 8 * 8; i += THREADS) {
-        const int j = i >> 3, c = i & 7;
-        const bool real = j < g.r;
-        cp_async16_if(ms + j * 128 + ((c ^ (j & 7)) << 4),
-                      ml + (size_t)(real ? j : 0) * g.D + kb * KC + c * 8, real);
+    for (int i = 0; i < 8; ++i) {
+      const int t = s_row[pr + 16 * i];
+      if (t >= 0) on |= 1u << i;
+      src[i] = g.in + (size_t)max(t, 0) * g.D + pc * 8;
+    }
+    const uint32_t dst0 = (uint32_t)(pr * 128 + ((pc ^ (pr & 7)) << 4));  // rows 16 apart: + 2 KB
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      int w = 0;
+      if (lane == 0)
+        w = mbar_wait(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit);
+      if (!__shfl_sync(0xffffffffu, w, 0)) {
+        ok = false;
+        break;
       }
-    } else {  // [KC][NT * 8]
-      for (int i = tid; i < KC * NT; i += THREADS) {
-        const int k = i / NT, c = i % NT;
-        const bool real = c * 8 < g.r;
-        cp_async16_if(ms + piece<NT>(k, c),
-                      ml + (size_t)(kb * KC + k) * g.r + (real ? c * 8 : 0), real);
+      const uint32_t xs = sb + stage * st_bytes + dst0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        cp_async16_if(xs + i * 2048, src[i] + (size_t)kb * KC, (on >> i & 1u) != 0);
+      cp_async_arrive_noinc(saddr(&full[stage]));
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
-  };
-  float acc[NT][4];
+    cp_async_wait_all();
+  } else if (warp == 4) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      // D fp32, A (rows) K-major bf16, B bf16: MN-major [k][r] or K-major [r][k] (TRANS)
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (TRANS ? 0u : 1u << 16) |
+                             ((uint32_t)(g.n_mma >> 3) << 17) | (8u << 24);
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(saddr(&full[stage]), phase, abort_flag, g.status, limit)) break;
+        fence_proxy_async_smem();  // the gathered rows (cp.async) -> MMA reads
+        tc_fence_after();
+        const uint32_t xs = sb + stage * st_bytes, ms = xs + X_BYTES;
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) {
-    if (kb0 + s < kb1) load(kb0 + s, s);
-    cp_async_commit();
-  }
-  for (int kb = kb0; kb < kb1; ++kb) {
-    cp_async_wait<STAGES - 2>();
-    __syncthreads();  // the stage has landed for every thread; the one before is free
-    if (kb + STAGES - 1 < kb1) load(kb + STAGES - 1, (kb - kb0 + STAGES - 1) % STAGES);
-    cp_async_commit();
-    const uint32_t xs = sb + ((kb - kb0) % STAGES) * ST, ms = xs + X_BYTES;
-#pragma unroll
-    for (int kk = 0; kk < KC / 16; ++kk) {
-      uint32_t a[4];
-      {
-        const int r = warp * 16 + (lane & 15), c = kk * 2 + (lane >> 4);
-        ldmatrix4(a, xs + r * 128 + ((c ^ (r & 7)) << 4));
-      }
-#pragma unroll
-      for (int i = 0; i < NT; i += 2) {
-        uint32_t b[4];
-        if (TRANS) {
-          const int j = i * 8 + (lane & 7) + ((lane >> 4) << 3), c = kk * 2 + ((lane >> 3) & 1);
-          ldmatrix4(b, ms + j * 128 + ((c ^ (j & 7)) << 4));
-        } else {
-          const int k = kk * 16 + (lane & 15), c = i + (lane >> 4);
-          ldmatrix4t(b, ms + piece<NT>(k, c));
+        for (int kk = 0; kk < KC / 16; ++kk)
+          tc_mma<1>(tmem, desc_sw128(xs + kk * 32, 16, 1024),
+                    TRANS ? desc_sw128(ms + kk * 32, 16, 1024)
+                          : desc_sw128(ms + kk * 2048, M_CHUNK, 1024),
+                    idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+        tc_commit<1>(saddr(&empty[stage]));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
-        mma16816(acc[i], a, b[0], b[1]);
-        mma16816(acc[i + 1], a, b[2], b[3]);
+      }
+      tc_commit<1>(saddr(&done));
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ the adapter's matrix (TMA)
+    int stage = 0;
+    uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
+      const uint32_t fb = saddr(&full[stage]), ms = sb + stage * st_bytes + X_BYTES;
+      mbar_expect_tx(fb, (uint32_t)(g.nc * M_CHUNK));
+      for (int c = 0; c < g.nc; ++c) {
+        if (TRANS) tma_load_3d(ms + c * M_CHUNK, &tmM, kb * KC, 64 * c, l, fb);
+        else tma_load_3d(ms + c * M_CHUNK, &tmM, 64 * c, kb * KC, l, fb);
+      }
+      issued_mask |= 1u << stage;
+      issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    for (int s = 0; s < STAGES; ++s) {  // nothing of ours is in flight after this (bounded)
+      if (!(issued_mask & (1u << s))) continue;
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try(saddr(&full[s]), (issued_par >> s) & 1u) && globaltimer_ns() - t0 < limit) {
       }
     }
   }
-  cp_async_wait<0>();
-  __syncthreads();
-  float* part = reinterpret_cast<float*>(smem);  // [ROWS][NT * 8]
-  {
-    const int r = warp * 16 + (lane >> 2), c = 2 * (lane & 3);
+  __syncwarp();
+  int w_ok = 0;
+  if (lane == 0) w_ok = mbar_wait(saddr(&done), 0, nullptr, g.status, limit);
+  ok = __shfl_sync(0xffffffffu, w_ok, 0) && ok;
+  tc_fence_before();
+  __syncthreads();  // every copy and MMA is done: the ring is free
+  tc_fence_after();
+  ok = ok && !*abort_flag;
+  // the partial in shared memory: [row][pitch], a thread its row
+  const int pitch = g.r + 4;
+  float* part = reinterpret_cast<float*>(base);
+  if (warp < 4) {
+    for (int j = 0; j < g.r; j += 8) {
+      uint32_t v[8];
+      if (kb0 < kb1) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+              "=r"(v[7])
+            : "r"(tmem + (uint32_t)j + ((uint32_t)(warp * 32) << 16)));
+        tmem_ld_wait();
+      } else {  // no k-block for this rank (d < 256)
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      *reinterpret_cast<float2*>(part + r * (NT * 8) + i * 8 + c) = make_float2(acc[i][0], acc[i][1]);
-      *reinterpret_cast<float2*>(part + (r + 8) * (NT * 8) + i * 8 + c) =
-          make_float2(acc[i][2], acc[i][3]);
+        for (int i = 0; i < 8; ++i) v[i] = 0u;
+      }
+      uint4* o = reinterpret_cast<uint4*>(part + (size_t)tid * pitch + j);
+      o[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      o[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
   }
+  tc_fence_before();
+  __syncwarp();
   cluster_sync();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, tcols);
+  }
   // this rank's share of the rows: the four partials in rank order
   const float sc = g.scale[l];
   uint32_t peer[SPLIT];
 #pragma unroll
   for (int q = 0; q < SPLIT; ++q) peer[q] = map_rank(sb, (uint32_t)q);
-  for (int i = tid; i < ROWS / SPLIT * (g.r / 2); i += THREADS) {
+  for (int i = tid; ok && i < ROWS / SPLIT * (g.r / 2); i += THREADS) {
     const int r = rank * (ROWS / SPLIT) + i / (g.r / 2), j = (i % (g.r / 2)) * 2;
     if (r >= n) continue;
-    const uint32_t at = (uint32_t)((r * (NT * 8) + j) * 4);
+    const uint32_t at = (uint32_t)((r * pitch + j) * 4);
     float v0 = 0.f, v1 = 0.f;
 #pragma unroll
     for (int q = 0; q < SPLIT; ++q) {
@@ -266,11 +324,23 @@ __global__ void __launch_bounds__(THREADS) adapter_low_kernel(const LowArgs g) {
   cluster_sync();  // no rank leaves while its partial may be read
 }
 
-template <bool TRANS, int NT>
-moe_status run_low(LowArgs a, cudaStream_t st) {
-  auto kern = adapter_low_kernel<TRANS, NT>;
-  const int smem = STAGES * (ROWS * KC * 2 + KC * NT * 16);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+template <bool TRANS>
+moe_status run_low(LowArgs a, const void* m, cudaStream_t st) {
+  auto kern = adapter_low_kernel<TRANS>;
+  a.n_mma = (a.r + 15) / 16 * 16;
+  a.nc = (a.r + 63) / 64;
+  a.status = device_status_ptr();
+  a.limit_ns = kWaitLimitNs;
+  CUtensorMap mm;
+  const uint64_t r = a.r, D = a.D, L = a.L;
+  const uint64_t md[3] = {TRANS ? D : r, TRANS ? r : D, L}, ms[2] = {md[0] * 2, D * r * 2};
+  const uint32_t mbox[3] = {64, 64, 1};
+  if (!make_map(&mm, m, 3, md, ms, mbox)) return MOE_ERR_CUDA;
+  int smem = STAGES * (X_BYTES + a.nc * M_CHUNK);
+  if (smem < ROWS * (a.r + 4) * 4) smem = ROWS * (a.r + 4) * 4;  // the partial
+  smem += 1024;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024) !=
+      cudaSuccess)
     return MOE_ERR_CUDA;
   // at most T / ROWS whole tiles and one ragged tile an adapter (or a row)
   const int ragged = a.L < a.T ? a.L : a.T;
@@ -278,19 +348,13 @@ moe_status run_low(LowArgs a, cudaStream_t st) {
   const int table = (a.T + SPLIT * kAdapterTileRows - 1) / (SPLIT * kAdapterTileRows);
   launch_begin(K_ADAPTER_LOW, st);
   launch_kernel(kern, dim3((unsigned)(SPLIT * (a.tile_clusters + table))), dim3(THREADS),
-                (size_t)smem, st, SPLIT, a);
+                (size_t)smem, st, SPLIT, mm, a);
   return launch_end(K_ADAPTER_LOW, st);
 }
 
-template <bool TRANS>
-moe_status run_low_nt(const LowArgs& a, cudaStream_t st) {
-  if (a.r <= 16) return run_low<TRANS, 2>(a, st);
-  if (a.r <= 32) return run_low<TRANS, 4>(a, st);
-  if (a.r <= 64) return run_low<TRANS, 8>(a, st);
-  return run_low<TRANS, 16>(a, st);
-}
-
 // ------------------------------------------------------------------ few rows
+constexpr int FEW_THREADS = 128;
+
 struct LowFewArgs {
   const bf16* x;
   const bf16* a;
@@ -303,20 +367,20 @@ struct LowFewArgs {
 };
 
 // CTA (row t, split s): eight rank values a thread, the contraction over the threads.
-__global__ void __launch_bounds__(THREADS) adapter_low_few_kernel(const LowFewArgs g) {
+__global__ void __launch_bounds__(FEW_THREADS) adapter_low_few_kernel(const LowFewArgs g) {
   __shared__ float xs[1024];
-  __shared__ float red[THREADS * 8];
+  __shared__ float red[FEW_THREADS * 8];
   const int tid = threadIdx.x, t = blockIdx.x, s = blockIdx.y;
   pdl_wait();  // the previous kernel in the stream has completed
   pdl_trigger();
   const int bid = blockIdx.y * gridDim.x + blockIdx.x, nb = gridDim.x * gridDim.y;
-  for (int i = bid * THREADS + tid; i < g.n_clear; i += nb * THREADS) g.clear[i] = 0u;
+  for (int i = bid * FEW_THREADS + tid; i < g.n_clear; i += nb * FEW_THREADS) g.clear[i] = 0u;
   const int l = g.ids[t];
   if (l < 0 || l >= g.L) {
     if (l != -1 && tid == 0 && s == 0) report(g.status, MOE_ERR_DEVICE_INDEX);
     return;  // nobody reads this row's partials
   }
-  const int rc = g.r / 8, step = THREADS / rc;
+  const int rc = g.r / 8, step = FEW_THREADS / rc;
   const int c = tid % rc, k_t = tid / rc;
   const int k0 = (int)((long long)s * (g.D / 8) / g.splits) * 8;
   const int k1 = (int)((long long)(s + 1) * (g.D / 8) / g.splits) * 8;
@@ -327,7 +391,7 @@ __global__ void __launch_bounds__(THREADS) adapter_low_few_kernel(const LowFewAr
   for (int kc = k0; kc < k1; kc += 1024) {
     const int nk = min(1024, k1 - kc);
     __syncthreads();
-    for (int i = tid * 8; i < nk; i += THREADS * 8) {
+    for (int i = tid * 8; i < nk; i += FEW_THREADS * 8) {
       float f[8];
       unpack16(*reinterpret_cast<const uint4*>(g.x + (size_t)t * g.D + kc + i), f, bf16());
 #pragma unroll
@@ -348,231 +412,37 @@ __global__ void __launch_bounds__(THREADS) adapter_low_few_kernel(const LowFewAr
 #pragma unroll
     for (int v = 0; v < 8; ++v) red[k_t * g.r + c * 8 + v] = acc[v];
   __syncthreads();
-  for (int j = tid; j < g.r; j += THREADS) {
+  for (int j = tid; j < g.r; j += FEW_THREADS) {
     float sum = 0.f;
     for (int q = 0; q < step; ++q) sum += red[q * g.r + j];
     g.part[((size_t)s * g.T + t) * g.r + j] = sum;
   }
 }
 
-// ------------------------------------------------------------------ outer products
-constexpr int OC = 128;   // columns of a unit: 32 a warp
-constexpr int OT = 32;    // rows per stage
-constexpr int OSTAGES = 3;
-
-struct OuterArgs {
-  const bf16* big[2];     // x [T, D0], d_y [T, D1]
-  const bf16* planes[2];  // [3][T][r] in slot order
-  float* out[2];          // dA [L, D0, r], dB [L, r, D1]
-  int D[2], tiles[2];     // widths and their 128-column tiles
-  const int32_t* offsets;
-  const int32_t* rows;
-  float* part;        // [chunk][D0 + D1][r]: adapters of several chunks
-  uint32_t* arrived;  // [L][tiles0 + tiles1], zero when the kernel starts
-  int T, r, L, chunk;
-};
-
-template <int NT>
-__global__ void __launch_bounds__(THREADS) adapter_outer_kernel(const OuterArgs g) {
-  constexpr int B_BYTES = OT * OC * 2, P_BYTES = OT * NT * 16, ST = B_BYTES + 3 * P_BYTES;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_l, s_i, s_n, s_base, s_last;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();  // the previous kernel in the stream has completed
-  pdl_trigger();
-  const int nct = g.tiles[0] + g.tiles[1];
-  const int cg = blockIdx.x / nct, ct = blockIdx.x % nct;  // chunk, column tile
-  if (tid == 0) s_l = -1;
-  __syncthreads();
-  if (warp == 0) {  // chunk cg: adapter, index in it, its chunks, first partial slot
-    int run = 0, mrun = 0;
-    for (int l0 = 0; l0 < g.L; l0 += 32) {
-      const int l = l0 + lane;
-      const int c = l < g.L ? g.offsets[l + 1] - g.offsets[l] : 0;
-      const int n = l < g.L ? max(1, (c + g.chunk - 1) / g.chunk) : 0;
-      const int m = n > 1 ? n : 0;
-      int incl = n, mincl = m;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        const int w = __shfl_up_sync(0xffffffffu, mincl, o);
-        if (lane >= o) {
-          incl += v;
-          mincl += w;
-        }
-      }
-      const int mine = run + incl - n;
-      if (cg >= mine && cg < mine + n) {
-        s_l = l;
-        s_i = cg - mine;
-        s_n = n;
-        s_base = mrun + mincl - m;
-      }
-      run += __shfl_sync(0xffffffffu, incl, 31);
-      mrun += __shfl_sync(0xffffffffu, mincl, 31);
-    }
-  }
-  __syncthreads();
-  const int l = s_l;
-  if (l < 0) return;
-  const int p = ct >= g.tiles[0] ? 1 : 0;
-  const int c0 = (ct - (p ? g.tiles[0] : 0)) * OC, D = g.D[p];
-  const int lo = g.offsets[l] + s_i * g.chunk;
-  const int n = max(0, min(g.chunk, g.offsets[l + 1] - lo));
-  const bf16* big = g.big[p];
-  const bf16* planes = g.planes[p];
-  const size_t plane = (size_t)g.T * g.r;
-  const uint32_t sb = saddr(smem);
-  const int cc = tid & 15, cr = tid >> 4;  // 16-byte piece of a row, rows cr + 8 i
-  const bool col_on = c0 + cc * 8 < D;
-  auto load = [&](int r0, int stage) {
-    const uint32_t bs = sb + stage * ST, ps = bs + B_BYTES;
-#pragma unroll
-    for (int i = 0; i < OT / 8; ++i) {
-      const int r = cr + 8 * i;
-      const bool on = r0 + r < n && col_on;
-      const int t = on ? g.rows[lo + r0 + r] : 0;
-      cp_async16_if(bs + r * 256 + ((cc ^ (r & 7)) << 4),
-                    big + (size_t)t * D + (on ? c0 + cc * 8 : 0), on);
-    }
-    for (int i = tid; i < 3 * OT * NT; i += THREADS) {
-      const int q = i / (OT * NT), r = i / NT % OT, c = i % NT;
-      const bool on = r0 + r < n && c * 8 < g.r;
-      cp_async16_if(ps + q * P_BYTES + piece<NT>(r, c),
-                    planes + q * plane + (on ? (size_t)(lo + r0 + r) * g.r + c * 8 : 0), on);
-    }
-  };
-  float acc[2][NT][4];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.f;
-  const int steps = (n + OT - 1) / OT;
-#pragma unroll
-  for (int s = 0; s < OSTAGES - 1; ++s) {
-    if (s < steps) load(s * OT, s);
-    cp_async_commit();
-  }
-  for (int s = 0; s < steps; ++s) {
-    cp_async_wait<OSTAGES - 2>();
-    __syncthreads();
-    if (s + OSTAGES - 1 < steps) load((s + OSTAGES - 1) * OT, (s + OSTAGES - 1) % OSTAGES);
-    cp_async_commit();
-    const uint32_t bs = sb + (s % OSTAGES) * ST, ps = bs + B_BYTES;
-#pragma unroll
-    for (int kk = 0; kk < OT / 16; ++kk) {
-      uint32_t a[2][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int k = kk * 16 + (lane & 7) + ((lane >> 4) << 3);
-        const int c = warp * 4 + m * 2 + ((lane >> 3) & 1);
-        ldmatrix4t(a[m], bs + k * 256 + ((c ^ (k & 7)) << 4));
-      }
-#pragma unroll
-      for (int q = 0; q < 3; ++q)
-#pragma unroll
-        for (int i = 0; i < NT; i += 2) {
-          uint32_t b[4];
-          ldmatrix4t(b, ps + q * P_BYTES + piece<NT>(kk * 16 + (lane & 15), i + (lane >> 4)));
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            mma16816(acc[m][i], a[m], b[0], b[1]);
-            mma16816(acc[m][i + 1], a[m], b[2], b[3]);
-          }
-        }
-    }
-  }
-  cp_async_wait<0>();
-  // rows of the accumulators are columns of `big`: c = c0 + 32 warp + 16 m + lane / 4 (+ 8)
-  const size_t wide = (size_t)(g.D[0] + g.D[1]);
-  const bool direct = s_n == 1;
-  float* part = direct ? nullptr
-                       : g.part + ((size_t)(s_base + s_i) * wide + (p ? g.D[0] : 0)) * g.r;
-  float* out = g.out[p] + (size_t)l * D * g.r;
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = c0 + warp * 32 + m * 16 + (lane >> 2) + 8 * h;
-      if (c >= D) continue;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int j = i * 8 + 2 * (lane & 3);
-        if (j >= g.r) continue;
-        const float v0 = acc[m][i][2 * h], v1 = acc[m][i][2 * h + 1];
-        if (!direct) {
-          *reinterpret_cast<float2*>(part + (size_t)c * g.r + j) = make_float2(v0, v1);
-        } else if (p == 0) {
-          *reinterpret_cast<float2*>(out + (size_t)c * g.r + j) = make_float2(v0, v1);
-        } else {
-          out[(size_t)j * D + c] = v0;
-          out[(size_t)(j + 1) * D + c] = v1;
-        }
-      }
-    }
-  if (direct) return;
-  // the adapter's last chunk to arrive adds them up, in chunk order
-  __threadfence();
-  __syncthreads();
-  if (tid == 0)
-    s_last = atomicAdd(g.arrived + (size_t)l * nct + ct, 1u) == (unsigned)(s_n - 1);
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  const float* p0 = g.part + ((size_t)s_base * wide + (p ? g.D[0] : 0)) * g.r;
-  const int w = min(OC, D - c0);
-  for (int i = tid; i < w * g.r; i += THREADS) {
-    // consecutive threads on consecutive outputs
-    const int c = c0 + (p == 0 ? i / g.r : i % w), j = p == 0 ? i % g.r : i / w;
-    float v = 0.f;
-    for (int q = 0; q < s_n; ++q) v += __ldcg(p0 + (size_t)q * wide * g.r + (size_t)c * g.r + j);
-    out[p == 0 ? (size_t)c * g.r + j : (size_t)j * D + c] = v;
-  }
-}
-
-template <int NT>
-moe_status run_outer(const OuterArgs& a, cudaStream_t st) {
-  auto kern = adapter_outer_kernel<NT>;
-  const int smem = OSTAGES * (OT * OC * 2 + 3 * OT * NT * 16);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  launch_begin(K_ADAPTER_OUTER, st);
-  launch_kernel(kern, dim3((unsigned)((a.T / a.chunk + a.L) * (a.tiles[0] + a.tiles[1]))),
-                dim3(THREADS), (size_t)smem, st, 1, a);
-  return launch_end(K_ADAPTER_OUTER, st);
-}
-
 }  // namespace
-
-// Rows of an outer-product unit: enough units for four a SM, at least 512 rows each.
-static int outer_chunk(int T, int d_in, int d_out) {
-  const long long tiles = (d_in + OC - 1) / OC + (d_out + OC - 1) / OC;
-  long long c = (long long)T * tiles / (4 * 148);
-  c = (c + 63) / 64 * 64;
-  return (int)(c < 512 ? 512 : c);
-}
-
-// Partial sums of adapters with more than one chunk: at most 2 T / chunk chunks.
-size_t adapter_outer_part_bytes(int T, int d_in, int d_out, int r) {
-  const size_t chunks = 2 * (size_t)(T / outer_chunk(T, d_in, d_out));
-  return chunks * (size_t)(d_in + d_out) * r * 4;
-}
-size_t adapter_outer_arrived_words(int d_in, int d_out, int L) {
-  return (size_t)L * ((d_in + OC - 1) / OC + (d_out + OC - 1) / OC);
-}
 
 moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void* in,
                               const void* m, const int32_t* ids, const int32_t* offsets,
                               const int32_t* rows, const float* scale, float* low, void* planes,
                               const float* low2, void* planes2, void* terms,
-                              AdapterTile* tiles, uint32_t* clear, int n_clear,
-                              cudaStream_t st) {
-  const LowArgs a{(const bf16*)in, (const bf16*)m,  ids,          offsets, rows, scale, low,
-                  (bf16*)planes,   low2,            (bf16*)planes2, (bf16*)terms, tiles, 0,
-                  clear,           n_clear,         T,            D,       r,    L};
-  return trans ? run_low_nt<true>(a, st) : run_low_nt<false>(a, st);
+                              AdapterTile* tiles, cudaStream_t st) {
+  LowArgs a = {};
+  a.in = (const bf16*)in;
+  a.ids = ids;
+  a.offsets = offsets;
+  a.rows = rows;
+  a.scale = scale;
+  a.low = low;
+  a.planes = (bf16*)planes;
+  a.low2 = low2;
+  a.planes2 = (bf16*)planes2;
+  a.terms = (bf16*)terms;
+  a.tiles = tiles;
+  a.T = T;
+  a.D = D;
+  a.r = r;
+  a.L = L;
+  return trans ? run_low<true>(a, m, st) : run_low<false>(a, m, st);
 }
 
 moe_status launch_adapter_low_few(int T, int D, int r, int L, int splits, const void* x,
@@ -581,39 +451,9 @@ moe_status launch_adapter_low_few(int T, int D, int r, int L, int splits, const 
   const LowFewArgs f{(const bf16*)x, (const bf16*)a, ids, part, clear, n_clear, T, D, r, L,
                      splits, device_status_ptr()};
   launch_begin(K_ADAPTER_LOW_FEW, st);
-  launch_kernel(adapter_low_few_kernel, dim3((unsigned)T, (unsigned)splits), dim3(THREADS), 0, st,
+  launch_kernel(adapter_low_few_kernel, dim3((unsigned)T, (unsigned)splits), dim3(FEW_THREADS), 0, st,
                 1, f);
   return launch_end(K_ADAPTER_LOW_FEW, st);
-}
-
-moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
-                                const void* d_y, const void* planes_d_low,
-                                const void* planes_low, const int32_t* offsets,
-                                const int32_t* rows, float* d_a, float* d_b, float* part,
-                                uint32_t* arrived, cudaStream_t st) {
-  OuterArgs a = {};
-  a.big[0] = (const bf16*)x;
-  a.big[1] = (const bf16*)d_y;
-  a.planes[0] = (const bf16*)planes_d_low;
-  a.planes[1] = (const bf16*)planes_low;
-  a.out[0] = d_a;
-  a.out[1] = d_b;
-  a.D[0] = d_in;
-  a.D[1] = d_out;
-  a.tiles[0] = (d_in + OC - 1) / OC;
-  a.tiles[1] = (d_out + OC - 1) / OC;
-  a.offsets = offsets;
-  a.rows = rows;
-  a.part = part;
-  a.arrived = arrived;
-  a.T = T;
-  a.r = r;
-  a.L = L;
-  a.chunk = outer_chunk(T, d_in, d_out);
-  if (r <= 16) return run_outer<2>(a, st);
-  if (r <= 32) return run_outer<4>(a, st);
-  if (r <= 64) return run_outer<8>(a, st);
-  return run_outer<16>(a, st);
 }
 
 }  // namespace moe

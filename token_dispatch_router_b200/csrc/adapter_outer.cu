@@ -1,0 +1,353 @@
+// Gradients of the adapter matrices: for each adapter l, over its rows t,
+//
+//   dA_l [d_in, r] = sum_t x[t]^T d_low[t],    dB_l [r, d_out] = sum_t low[t]^T d_y[t]
+//
+// Bound by reading the wide rows of x and d_y once. Rows come in any order, so they are
+// gathered by cp.async into the swizzled layout that the tensor cores read; both operands are
+// taken as they lie (a row is one k of the product: MN-major), so nothing is transposed. M is
+// the wide side (256 columns a unit, two accumulators), N the rank (16 ... 128), K the rows.
+// The low-rank side is fp32: it enters as three bf16 terms accumulated one after another, exact
+// to 2^-24, so the fp32 gradients lose nothing; the tensor pipe has the time (three MMAs of
+// N = r for each 32 x 256 tile of wide rows).
+//
+// A unit is (adapter, chunk of its rows, 256 columns of x or of d_y); several are resident on an
+// SM so that one loads while another stores. Chunks of one adapter leave partial sums that a
+// second kernel adds in chunk order (results repeat bit for bit); it is launched only where an
+// adapter can have two chunks. An adapter without rows has one empty chunk, which writes zeros.
+// Every wait is bounded (MOE_ERR_TIMEOUT on expiry).
+#include "adapter.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace ptx;
+
+constexpr int LOADERS = 128, THREADS = 160;  // four load / store warps, one MMA warp
+constexpr int OC = 256;                      // columns of a unit
+constexpr int OT = 32;                       // rows per stage
+constexpr int STAGES = 3;
+constexpr int CHUNK = OT * 128;              // OT rows x 64 columns
+constexpr int BIG_BYTES = OC / 64 * CHUNK;   // 16 KB
+
+struct OuterArgs {
+  const bf16* big[2];     // x [T, D0], d_y [T, D1]
+  const bf16* planes[2];  // d_low, low: [3][T][r] in slot order
+  float* out[2];          // dA [L, D0, r], dB [L, r, D1]
+  int D[2], tiles[2];     // widths and their 256-column tiles
+  const int32_t* offsets;
+  const int32_t* rows;
+  float* part;        // [chunk][(D0 + D1) r]: adapters of several chunks
+  int T, r, L, chunk;
+  int n_mma;          // the rank rounded up to 16
+  int nc;             // its 64-column pieces
+  unsigned* status;
+  unsigned long long limit_ns;
+};
+
+__global__ void __launch_bounds__(THREADS) adapter_outer_kernel(const OuterArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[STAGES], empty[STAGES], done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_l, s_i, s_n, s_base, s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sb = (saddr(smem_raw) + 1023u) & ~1023u;
+  const int p_bytes = g.nc * CHUNK, st_bytes = BIG_BYTES + 3 * p_bytes;
+  volatile int* abort_flag = &s_abort;
+  uint32_t tcols = 32;
+  while ((int)tcols < 2 * g.n_mma) tcols *= 2;
+
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(saddr(&full[s]), LOADERS);
+      mbar_init(saddr(&empty[s]), 1);
+    }
+    mbar_init(saddr(&done), 1);
+    s_abort = 0;
+    s_l = -1;
+    mbar_init_fence();
+  }
+  __syncthreads();
+  pdl_wait();  // the previous kernel in the stream has completed
+  pdl_trigger();
+  const int nct = g.tiles[0] + g.tiles[1];
+  const int cg = blockIdx.x / nct, ct = blockIdx.x % nct;  // chunk, column tile
+  if (warp == 0) {  // chunk cg: adapter, index in it, its chunks, first partial slot
+    int run = 0, mrun = 0;
+    for (int l0 = 0; l0 < g.L; l0 += 32) {
+      const int l = l0 + lane;
+      const int c = l < g.L ? g.offsets[l + 1] - g.offsets[l] : 0;
+      const int n = l < g.L ? max(1, (c + g.chunk - 1) / g.chunk) : 0;
+      const int m = n > 1 ? n : 0;
+      int incl = n, mincl = m;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int w = __shfl_up_sync(0xffffffffu, mincl, o);
+        if (lane >= o) {
+          incl += v;
+          mincl += w;
+        }
+      }
+      const int mine = run + incl - n;
+      if (cg >= mine && cg < mine + n) {
+        s_l = l;
+        s_i = cg - mine;
+        s_n = n;
+        s_base = mrun + mincl - m;
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
+      mrun += __shfl_sync(0xffffffffu, mincl, 31);
+    }
+  }
+  __syncthreads();
+  const int l = s_l;
+  if (l < 0) return;  // past the last chunk
+  if (warp == 4) tmem_alloc<1>(saddr(&s_tmem), tcols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int p = ct >= g.tiles[0] ? 1 : 0;
+  const int c0 = (ct - (p ? g.tiles[0] : 0)) * OC, D = g.D[p];
+  const int lo = g.offsets[l] + s_i * g.chunk;
+  const int n = max(0, min(g.chunk, g.offsets[l + 1] - lo));
+  const int steps = (n + OT - 1) / OT;
+  const uint64_t limit = g.limit_ns;
+  bool ok = true;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ gather
+    // wide rows: warp w copies rows w, w + 4, ..., 512 bytes (one 16-byte piece a lane) each
+    const bf16* big = g.big[p] + c0 + lane * 8;
+    const bool col_on = c0 + lane * 8 < D;
+    const int chunk_at = (lane >> 3) * CHUNK;
+    const bf16* planes = g.planes[p];
+    const size_t plane = (size_t)g.T * g.r;
+    const int pieces = g.n_mma / 8;
+    // lane i < 8 holds the row of this warp's i-th row in the next stage
+    auto row_of = [&](int s) {
+      const int r = s * OT + warp + 4 * (lane & 7);
+      return r < n ? g.rows[lo + r] : -1;
+    };
+    int ahead = steps > 0 ? row_of(0) : -1;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int s = 0; s < steps; ++s) {
+      const int mine = ahead;
+      if (s + 1 < steps) ahead = row_of(s + 1);
+      int w = 0;
+      if (lane == 0)
+        w = mbar_wait(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit);
+      if (!__shfl_sync(0xffffffffu, w, 0)) {
+        ok = false;
+        break;
+      }
+      const uint32_t bs = sb + stage * st_bytes, ps = bs + BIG_BYTES;
+#pragma unroll
+      for (int i = 0; i < OT / 4; ++i) {
+        const int t = __shfl_sync(0xffffffffu, mine, i), r = warp + 4 * i;
+        const bool on = t >= 0 && col_on;
+        cp_async16_if(bs + chunk_at + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                      on ? big + (size_t)t * D : g.big[p], on);
+      }
+      for (int i = tid; i < 3 * OT * pieces; i += LOADERS) {
+        const int q = i / (OT * pieces), r = i / pieces % OT, c = i % pieces;
+        const bool on = s * OT + r < n && c * 8 < g.r;
+        cp_async16_if(ps + q * p_bytes + (c >> 3) * CHUNK + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                      planes + (on ? q * plane + (size_t)(lo + s * OT + r) * g.r + c * 8 : 0), on);
+      }
+      cp_async_arrive_noinc(saddr(&full[stage]));
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    cp_async_wait_all();
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    // D fp32, A and B bf16, both MN-major (bits 15 and 16), M = 128, N = n_mma
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
+                           ((uint32_t)(g.n_mma >> 3) << 17) | (8u << 24);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int s = 0; s < steps; ++s) {
+      if (!mbar_wait(saddr(&full[stage]), phase, abort_flag, g.status, limit)) break;
+      fence_proxy_async_smem();  // the gathered rows (cp.async) -> MMA reads
+      tc_fence_after();
+      const uint32_t bs = sb + stage * st_bytes, ps = bs + BIG_BYTES;
+#pragma unroll
+      for (int kk = 0; kk < OT / 16; ++kk)
+        for (int q = 0; q < 3; ++q) {
+          const uint64_t bd = desc_sw128(ps + q * p_bytes + kk * 2048, CHUNK, 1024);
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            tc_mma<1>(tmem + (uint32_t)(m * g.n_mma),
+                      desc_sw128(bs + m * 2 * CHUNK + kk * 2048, CHUNK, 1024), bd, idesc,
+                      (s | kk | q) != 0 ? 1u : 0u);
+        }
+      tc_commit<1>(saddr(&empty[stage]));
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    tc_commit<1>(saddr(&done));
+  }
+  __syncwarp();
+  int w_ok = 0;
+  if (lane == 0) w_ok = mbar_wait(saddr(&done), 0, nullptr, g.status, limit);
+  ok = __shfl_sync(0xffffffffu, w_ok, 0) && ok && !*abort_flag;
+  tc_fence_after();
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ store
+    const size_t wide = (size_t)(g.D[0] + g.D[1]) * g.r, at = p ? (size_t)g.D[0] * g.r : 0;
+    const bool direct = s_n == 1;
+    float* out = g.out[p] + (size_t)l * D * g.r;
+    float* dst = direct ? out : g.part + (size_t)(s_base + s_i) * wide + at;
+#pragma unroll 1
+    for (int m = 0; m < 2; ++m) {
+      const int c = c0 + m * 128 + warp * 32 + lane;
+#pragma unroll 1
+      for (int j0 = 0; j0 < g.r; j0 += 8) {
+        uint32_t v[8];
+        if (steps > 0) {
+          asm volatile(
+              "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+              : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                "=r"(v[6]), "=r"(v[7])
+              : "r"(tmem + (uint32_t)(m * g.n_mma + j0) + ((uint32_t)(warp * 32) << 16)));
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = 0u;
+        }
+        if (c >= D || !ok) continue;
+        if (p == 0) {
+          uint4* o = reinterpret_cast<uint4*>(dst + (size_t)c * g.r + j0);
+          o[0] = make_uint4(v[0], v[1], v[2], v[3]);
+          o[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dst[(size_t)(j0 + j) * D + c] = __uint_as_float(v[j]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, tcols);
+  }
+}
+
+// dA and dB of the adapters with several chunks: their partial sums in chunk order. CTA (piece,
+// adapter): 4096 of the adapter's (D0 + D1) r values.
+constexpr int SUM_THREADS = 256, SUM_PIECE = 4 * 4 * SUM_THREADS;
+__global__ void __launch_bounds__(SUM_THREADS) adapter_outer_sum_kernel(const OuterArgs g) {
+  __shared__ int s_before[SUM_THREADS / 32];
+  pdl_wait();  // the previous kernel in the stream has completed
+  pdl_trigger();
+  const int tid = threadIdx.x, l = blockIdx.y;
+  auto chunks = [&](int a) {
+    const int n = (g.offsets[a + 1] - g.offsets[a] + g.chunk - 1) / g.chunk;
+    return n > 1 ? n : 0;
+  };
+  const int n = chunks(l);
+  if (n == 0) return;
+  int before = tid < l ? chunks(tid) : 0;  // L <= 256
+  before = __reduce_add_sync(0xffffffffu, before);
+  if ((tid & 31) == 0) s_before[tid >> 5] = before;
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i < SUM_THREADS / 32; ++i) base += s_before[i];
+  const size_t na = (size_t)g.D[0] * g.r, wide = na + (size_t)g.D[1] * g.r;
+  const float* p0 = g.part + (size_t)base * wide;
+  float4 v[4];
+  size_t at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    at[i] = (size_t)blockIdx.x * SUM_PIECE + (size_t)(i * SUM_THREADS + tid) * 4;
+    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 2
+  for (int q = 0; q < n; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at[i] < wide) {
+        const float4 u = *reinterpret_cast<const float4*>(p0 + (size_t)q * wide + at[i]);
+        v[i].x += u.x; v[i].y += u.y; v[i].z += u.z; v[i].w += u.w;
+      }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (at[i] < wide)  // D0 r is a multiple of four: a vector lies in one of the two
+      *reinterpret_cast<float4*>(at[i] < na
+                                     ? g.out[0] + (size_t)l * na + at[i]
+                                     : g.out[1] + (size_t)l * (wide - na) + (at[i] - na)) = v[i];
+}
+
+int tiles_of(int d) { return (d + OC - 1) / OC; }
+
+// Rows of a unit: enough units for two a SM, at least 512 rows each.
+int chunk_of(int T, int d_in, int d_out) {
+  long long c = (long long)T * (tiles_of(d_in) + tiles_of(d_out)) / (2 * 148);
+  c = (c + 63) / 64 * 64;
+  return (int)(c < 512 ? 512 : c);
+}
+
+}  // namespace
+
+// Partial sums of adapters with more than one chunk: at most 2 T / chunk chunks.
+size_t adapter_outer_part_bytes(int T, int d_in, int d_out, int r) {
+  const size_t chunks = 2 * (size_t)(T / chunk_of(T, d_in, d_out));
+  return chunks * (size_t)(d_in + d_out) * r * 4;
+}
+
+moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
+                                const void* d_y, const void* planes_d_low,
+                                const void* planes_low, const int32_t* offsets,
+                                const int32_t* rows, float* d_a, float* d_b, float* part,
+                                cudaStream_t st) {
+  OuterArgs a = {};
+  a.big[0] = (const bf16*)x;
+  a.big[1] = (const bf16*)d_y;
+  a.planes[0] = (const bf16*)planes_d_low;
+  a.planes[1] = (const bf16*)planes_low;
+  a.out[0] = d_a;
+  a.out[1] = d_b;
+  a.D[0] = d_in;
+  a.D[1] = d_out;
+  a.tiles[0] = tiles_of(d_in);
+  a.tiles[1] = tiles_of(d_out);
+  a.offsets = offsets;
+  a.rows = rows;
+  a.part = part;
+  a.T = T;
+  a.r = r;
+  a.L = L;
+  a.chunk = chunk_of(T, d_in, d_out);
+  a.n_mma = (r + 15) / 16 * 16;
+  a.nc = (r + 63) / 64;
+  a.status = device_status_ptr();
+  a.limit_ns = kWaitLimitNs;
+  const int smem = 1024 + STAGES * (BIG_BYTES + 3 * a.nc * CHUNK);
+  if (cudaFuncSetAttribute(adapter_outer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           160 * 1024) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  launch_begin(K_ADAPTER_OUTER, st);
+  launch_kernel(adapter_outer_kernel, dim3((unsigned)((T / a.chunk + L) * (a.tiles[0] + a.tiles[1]))),
+                dim3(THREADS), (size_t)smem, st, 1, a);
+  const moe_status s = launch_end(K_ADAPTER_OUTER, st);
+  if (s != MOE_OK || T <= a.chunk) return s;
+  const size_t wide = (size_t)(d_in + d_out) * r;
+  launch_begin(K_ADAPTER_OUTER_SUM, st);
+  launch_kernel(adapter_outer_sum_kernel,
+                dim3((unsigned)((wide + SUM_PIECE - 1) / SUM_PIECE), (unsigned)L),
+                dim3(SUM_THREADS), 0, st, 1, a);
+  return launch_end(K_ADAPTER_OUTER_SUM, st);
+}
+
+}  // namespace moe

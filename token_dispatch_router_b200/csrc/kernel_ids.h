@@ -44,6 +44,7 @@ enum KernelId {
   K_ADAPTER_LOW,
   K_ADAPTER_GEMM,
   K_ADAPTER_OUTER,
+  K_ADAPTER_OUTER_SUM,
   K_COUNT
 };
 
