@@ -16,6 +16,7 @@
 // adapter can have two chunks. An adapter without rows has one empty chunk, which writes zeros.
 // Every wait is bounded (MOE_ERR_TIMEOUT on expiry).
 #include "adapter.cuh"
+#include "ffn_args.cuh"
 
 namespace moe {
 
@@ -23,7 +24,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int LOADERS = 128, THREADS = 160;  // four load / store warps, one MMA warp
+constexpr int LOADERS = 128, THREADS = 192;  // four gather / store warps, MMA warp, TMA warp
 constexpr int OC = 256;                      // columns of a unit
 constexpr int OT = 32;                       // rows per stage
 constexpr int STAGES = 3;
@@ -45,7 +46,9 @@ struct OuterArgs {
   unsigned long long limit_ns;
 };
 
-__global__ void __launch_bounds__(THREADS) adapter_outer_kernel(const OuterArgs g) {
+__global__ void __launch_bounds__(THREADS)
+    adapter_outer_kernel(const __grid_constant__ CUtensorMap tmP0,
+                         const __grid_constant__ CUtensorMap tmP1, const OuterArgs g) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[STAGES], empty[STAGES], done;
   __shared__ uint32_t s_tmem;
@@ -59,7 +62,7 @@ __global__ void __launch_bounds__(THREADS) adapter_outer_kernel(const OuterArgs 
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(saddr(&full[s]), LOADERS);
+      mbar_init(saddr(&full[s]), LOADERS + 1);
       mbar_init(saddr(&empty[s]), 1);
     }
     mbar_init(saddr(&done), 1);
@@ -151,12 +154,14 @@ __global__ void __launch_bounds__(THREADS) adapter_outer_kernel(const OuterArgs 
         cp_async16_if(bs + chunk_at + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
                       on ? big + (size_t)t * D : g.big[p], on);
       }
-      for (int i = tid; i < 3 * OT * pieces; i += LOADERS) {
-        const int q = i / (OT * pieces), r = i / pieces % OT, c = i % pieces;
-        const bool on = s * OT + r < n && c * 8 < g.r;
-        cp_async16_if(ps + q * p_bytes + (c >> 3) * CHUNK + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                      planes + (on ? q * plane + (size_t)(lo + s * OT + r) * g.r + c * 8 : 0), on);
-      }
+      if ((s + 1) * OT > n)  // the last rows: the slots behind them are another adapter's
+        for (int i = tid; i < 3 * OT * pieces; i += LOADERS) {
+          const int q = i / (OT * pieces), r = i / pieces % OT, c = i % pieces;
+          const bool on = s * OT + r < n && c * 8 < g.r;
+          cp_async16_if(ps + q * p_bytes + (c >> 3) * CHUNK + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                        planes + (on ? q * plane + (size_t)(lo + s * OT + r) * g.r + c * 8 : 0),
+                        on);
+        }
       cp_async_arrive_noinc(saddr(&full[stage]));
       if (++stage == STAGES) {
         stage = 0;
@@ -164,6 +169,38 @@ __global__ void __launch_bounds__(THREADS) adapter_outer_kernel(const OuterArgs 
       }
     }
     cp_async_wait_all();
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ low-rank terms (TMA)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+      for (int s = 0; s < steps; ++s) {
+        if (!mbar_wait(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
+        const uint32_t fb = saddr(&full[stage]), ps = sb + stage * st_bytes + BIG_BYTES;
+        if ((s + 1) * OT <= n) {
+          mbar_expect_tx(fb, (uint32_t)(3 * p_bytes));
+          for (int q = 0; q < 3; ++q)
+            for (int c = 0; c < g.nc; ++c)
+              tma_load_3d(ps + q * p_bytes + c * CHUNK, p ? &tmP1 : &tmP0, 64 * c, lo + s * OT, q,
+                          fb);
+        } else {
+          mbar_arrive(fb);  // the gather warps copy these
+        }
+        issued_mask |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      for (int s = 0; s < STAGES; ++s) {  // nothing of ours is in flight after this (bounded)
+        if (!(issued_mask & (1u << s))) continue;
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try(saddr(&full[s]), (issued_par >> s) & 1u) &&
+               globaltimer_ns() - t0 < limit) {
+        }
+      }
+    }
   } else if (lane == 0) {
     // ------------------------------------------------------------ MMA issuer
     // D fp32, A and B bf16, both MN-major (bits 15 and 16), M = 128, N = n_mma
@@ -291,9 +328,9 @@ __global__ void __launch_bounds__(SUM_THREADS) adapter_outer_sum_kernel(const Ou
 
 int tiles_of(int d) { return (d + OC - 1) / OC; }
 
-// Rows of a unit: enough units for two a SM, at least 512 rows each.
+// Rows of a unit: enough units for four a SM, at least 512 rows each.
 int chunk_of(int T, int d_in, int d_out) {
-  long long c = (long long)T * (tiles_of(d_in) + tiles_of(d_out)) / (2 * 148);
+  long long c = (long long)T * (tiles_of(d_in) + tiles_of(d_out)) / (4 * 148);
   c = (c + 63) / 64 * 64;
   return (int)(c < 512 ? 512 : c);
 }
@@ -337,9 +374,14 @@ moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const 
   if (cudaFuncSetAttribute(adapter_outer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            160 * 1024) != cudaSuccess)
     return MOE_ERR_CUDA;
+  CUtensorMap m0, m1;
+  const uint64_t pd[3] = {(uint64_t)r, (uint64_t)T, 3}, ps[2] = {pd[0] * 2, pd[0] * pd[1] * 2};
+  const uint32_t pbox[3] = {64, OT, 1};
+  if (!make_map(&m0, planes_d_low, 3, pd, ps, pbox) || !make_map(&m1, planes_low, 3, pd, ps, pbox))
+    return MOE_ERR_CUDA;
   launch_begin(K_ADAPTER_OUTER, st);
   launch_kernel(adapter_outer_kernel, dim3((unsigned)((T / a.chunk + L) * (a.tiles[0] + a.tiles[1]))),
-                dim3(THREADS), (size_t)smem, st, 1, a);
+                dim3(THREADS), (size_t)smem, st, 1, m0, m1, a);
   const moe_status s = launch_end(K_ADAPTER_OUTER, st);
   if (s != MOE_OK || T <= a.chunk) return s;
   const size_t wide = (size_t)(d_in + d_out) * r;
