@@ -1,6 +1,6 @@
 // Host side of the adapter products: workspace layouts and launch sequences.
 //
-//   forward,  at most 128 rows: low partials -> the few-token product kernel (two launches)
+//   forward,  at most 128 rows: low partials -> the few-token second product (two launches)
 //   forward,  more rows:        group rows by adapter -> low -> product with the adapter term
 //   backward:                   group -> d_low -> d_x product with the adapter term
 //                               -> outer products d_A, d_B
@@ -8,6 +8,7 @@
 // with id -1 belongs to none.
 #include "adapter.cuh"
 #include "few.cuh"
+#include "few_args.cuh"
 
 namespace moe {
 
@@ -15,15 +16,11 @@ size_t permute_scratch_bytes(const moe_shape& s);
 moe_status launch_permute(const moe_shape& s, const int32_t* ids, int32_t* counts,
                           int32_t* offsets, int32_t* a2p, int32_t* p2a, const void* x,
                           void* x_perm, void* scratch, cudaStream_t st);
-int adapter_few_splits(int T, int d_out);
-moe_status launch_adapter_few(int T, int d_in, int d_out, int n_adapters, int rank, const void* x,
-                              const void* w, const void* b, const int32_t* ids,
-                              const float* scale, const float* low_part, int low_splits,
-                              float* low, void* y, float* y32, int smax, uint32_t* ctl,
+moe_status launch_adapter_few(FewDownArgs a, int d_in, const void* x, const void* w,
                               cudaStream_t st);
 moe_status launch_adapter_low_few(int T, int D, int r, int L, int splits, const void* x,
                                   const void* a, const int32_t* ids, float* part,
-                                  uint32_t* clear, int n_clear, cudaStream_t st);
+                                  cudaStream_t st);
 moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void* in,
                               const void* m, const int32_t* ids, const int32_t* offsets,
                               const int32_t* rows, const float* scale, float* low, void* planes,
@@ -58,24 +55,6 @@ moe_shape group_shape(const moe_adapter_shape& s) {
   g.K = 1;
   g.dtype = MOE_BF16;
   return g;
-}
-
-struct FewLayout {
-  size_t ctl, low_part, y32, total;
-  int smax;
-};
-FewLayout few_layout(const moe_adapter_shape& s) {
-  FewLayout L;
-  size_t o = 0;
-  L.ctl = o;
-  o = up256(o + kFewCtlWords * 4);
-  L.low_part = o;
-  o = up256(o + (size_t)low_few_splits(s) * s.T * s.rank * 4);
-  L.y32 = o;
-  L.smax = adapter_few_splits(s.T, s.d_out);
-  o = up256(o + (size_t)L.smax * s.T * s.d_out * 4);
-  L.total = o;
-  return L;
 }
 
 struct Layout {
@@ -118,7 +97,8 @@ moe_status group(const moe_adapter_shape& s, const int32_t* ids, const Layout& L
 }  // namespace
 
 size_t adapter_forward_bytes(const moe_adapter_shape& s) {
-  return s.T <= kFewMaxTokens ? few_layout(s).total : layout(s).total_fwd;
+  return s.T <= kFewMaxTokens ? up256((size_t)low_few_splits(s) * s.T * s.rank * 4)
+                              : layout(s).total_fwd;
 }
 size_t adapter_backward_bytes(const moe_adapter_shape& s) { return layout(s).total; }
 
@@ -128,15 +108,25 @@ moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, con
                                   cudaStream_t st) {
   moe_status r;
   if (s.T <= kFewMaxTokens) {
-    const FewLayout L = few_layout(s);
-    const int splits = low_few_splits(s);
-    uint32_t* ctl = (uint32_t*)(ws + L.ctl);
-    float* part = (float*)(ws + L.low_part);
-    if ((r = launch_adapter_low_few(s.T, s.d_in, s.rank, s.n_adapters, splits, x, a, ids, part,
-                                    ctl, kFewCtlWords, st)) != MOE_OK)
+    FewDownArgs f = {};
+    f.T = s.T;
+    f.K = 1;
+    f.E = 1;
+    f.cap = s.T;
+    f.d = s.d_out;
+    f.ids = ids;
+    f.out = (bf16*)y;
+    f.low_part = (const float*)ws;
+    f.low = low;
+    f.b = (const bf16*)b;
+    f.scale = scale;
+    f.rank = s.rank;
+    f.low_splits = low_few_splits(s);
+    f.n_adapters = s.n_adapters;
+    if ((r = launch_adapter_low_few(s.T, s.d_in, s.rank, s.n_adapters, f.low_splits, x, a, ids,
+                                    (float*)ws, st)) != MOE_OK)
       return r;
-    return launch_adapter_few(s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w, b, ids, scale,
-                              part, splits, low, y, (float*)(ws + L.y32), L.smax, ctl, st);
+    return launch_adapter_few(f, s.d_in, x, w, st);
   }
   const Layout L = layout(s);
   if ((r = group(s, ids, L, ws, st)) != MOE_OK) return r;

@@ -2,8 +2,7 @@
 //
 //   grouped:  low[t] = scale_l in[t] M_l, l = ids[t], for rows grouped by adapter
 //             (forward: in = x, M = A_l [d_in, r]; backward: in = d_y, M = B_l^T, B_l [r, d_out])
-//   few:      partial sums of x[t] A_l for at most 128 rows, and the control words of the
-//             kernel that follows
+//   few:      partial sums of x[t] A_l for at most 128 rows
 //
 // Bound by reading the wide rows once. The grouped form gives a cluster of four CTAs up to 128
 // rows of one adapter (grouping is the layer's stable permutation, so a tile never mixes
@@ -120,8 +119,11 @@ __global__ void __launch_bounds__(THREADS)
   const uint32_t sb = saddr(base);
   const int st_bytes = X_BYTES + g.nc * M_CHUNK;
   volatile int* abort_flag = &s_abort;
+  // MMAs into one accumulator follow each other about 190 cycles apart however small they are:
+  // the k steps go round four accumulators (two of a rank above 64)
+  const int accs = g.nc == 1 ? 4 : 2;
   uint32_t tcols = 32;
-  while ((int)tcols < g.n_mma) tcols *= 2;
+  while ((int)tcols < accs * g.n_mma) tcols *= 2;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(saddr(&full[s]), LOADERS + 1);
@@ -178,10 +180,7 @@ __global__ void __launch_bounds__(THREADS)
     int stage = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-      int w = 0;
-      if (lane == 0)
-        w = mbar_wait(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit);
-      if (!__shfl_sync(0xffffffffu, w, 0)) {
+      if (!mbar_wait_warp(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) {
         ok = false;
         break;
       }
@@ -197,32 +196,35 @@ __global__ void __launch_bounds__(THREADS)
     }
     cp_async_wait_all();
   } else if (warp == 4) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
-      // D fp32, A (rows) K-major bf16, B bf16: MN-major [k][r] or K-major [r][k] (TRANS)
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (TRANS ? 0u : 1u << 16) |
-                             ((uint32_t)(g.n_mma >> 3) << 17) | (8u << 24);
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(saddr(&full[stage]), phase, abort_flag, g.status, limit)) break;
-        fence_proxy_async_smem();  // the gathered rows (cp.async) -> MMA reads
-        tc_fence_after();
-        const uint32_t xs = sb + stage * st_bytes, ms = xs + X_BYTES;
+    // ------------------------------------------------------------ MMA issuer
+    // D fp32, A (rows) K-major bf16, B bf16: MN-major [k][r] or K-major [r][k] (TRANS)
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (TRANS ? 0u : 1u << 16) |
+                           ((uint32_t)(g.n_mma >> 3) << 17) | (8u << 24);
+    const uint64_t xd0 = desc_sw128(sb, 16, 1024);
+    const uint64_t md0 = TRANS ? desc_sw128(sb + X_BYTES, 16, 1024)
+                               : desc_sw128(sb + X_BYTES, M_CHUNK, 1024);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait_warp(saddr(&full[stage]), phase, abort_flag, g.status, limit)) break;
+      fence_proxy_async_smem();  // the gathered rows (cp.async) -> MMA reads
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t so = (uint64_t)((stage * st_bytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < KC / 16; ++kk)
-          tc_mma<1>(tmem, desc_sw128(xs + kk * 32, 16, 1024),
-                    TRANS ? desc_sw128(ms + kk * 32, 16, 1024)
-                          : desc_sw128(ms + kk * 2048, M_CHUNK, 1024),
-                    idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+          tc_mma<1>(tmem + (uint32_t)((kk & (accs - 1)) * g.n_mma), xd0 + so + (uint64_t)(kk * 2),
+                    md0 + so + (uint64_t)(kk * (TRANS ? 2 : 128)), idesc,
+                    (kb > kb0 || kk >= accs) ? 1u : 0u);
         tc_commit<1>(saddr(&empty[stage]));
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      tc_commit<1>(saddr(&done));
+      __syncwarp();
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
+    if (elect_one()) tc_commit<1>(saddr(&done));
   } else if (lane == 0) {
     // ------------------------------------------------------------ the adapter's matrix (TMA)
     int stage = 0;
@@ -262,21 +264,20 @@ __global__ void __launch_bounds__(THREADS)
   float* part = reinterpret_cast<float*>(base);
   if (warp < 4) {
     for (int j = 0; j < g.r; j += 8) {
-      uint32_t v[8];
-      if (kb0 < kb1) {
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-              "=r"(v[7])
-            : "r"(tmem + (uint32_t)j + ((uint32_t)(warp * 32) << 16)));
-        tmem_ld_wait();
-      } else {  // no k-block for this rank (d < 256)
+      float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0u;
-      }
-      uint4* o = reinterpret_cast<uint4*>(part + (size_t)tid * pitch + j);
-      o[0] = make_uint4(v[0], v[1], v[2], v[3]);
-      o[1] = make_uint4(v[4], v[5], v[6], v[7]);
+      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+      if (kb0 < kb1)  // else no k-block for this rank (d < 256)
+        for (int c = 0; c < accs; ++c) {
+          uint32_t v[8];
+          tmem_ld8(tmem + (uint32_t)(c * g.n_mma + j) + ((uint32_t)(warp * 32) << 16), v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] += __uint_as_float(v[i]);
+        }
+      float4* o = reinterpret_cast<float4*>(part + (size_t)tid * pitch + j);
+      o[0] = make_float4(f[0], f[1], f[2], f[3]);
+      o[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
   }
   tc_fence_before();
@@ -360,8 +361,6 @@ struct LowFewArgs {
   const bf16* a;
   const int32_t* ids;
   float* part;  // [splits][T][r]
-  uint32_t* clear;
-  int n_clear;
   int T, D, r, L, splits;
   unsigned* status;
 };
@@ -373,8 +372,6 @@ __global__ void __launch_bounds__(FEW_THREADS) adapter_low_few_kernel(const LowF
   const int tid = threadIdx.x, t = blockIdx.x, s = blockIdx.y;
   pdl_wait();  // the previous kernel in the stream has completed
   pdl_trigger();
-  const int bid = blockIdx.y * gridDim.x + blockIdx.x, nb = gridDim.x * gridDim.y;
-  for (int i = bid * FEW_THREADS + tid; i < g.n_clear; i += nb * FEW_THREADS) g.clear[i] = 0u;
   const int l = g.ids[t];
   if (l < 0 || l >= g.L) {
     if (l != -1 && tid == 0 && s == 0) report(g.status, MOE_ERR_DEVICE_INDEX);
@@ -447,9 +444,9 @@ moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void
 
 moe_status launch_adapter_low_few(int T, int D, int r, int L, int splits, const void* x,
                                   const void* a, const int32_t* ids, float* part,
-                                  uint32_t* clear, int n_clear, cudaStream_t st) {
-  const LowFewArgs f{(const bf16*)x, (const bf16*)a, ids, part, clear, n_clear, T, D, r, L,
-                     splits, device_status_ptr()};
+                                  cudaStream_t st) {
+  const LowFewArgs f{(const bf16*)x, (const bf16*)a, ids, part, T, D, r, L, splits,
+                     device_status_ptr()};
   launch_begin(K_ADAPTER_LOW_FEW, st);
   launch_kernel(adapter_low_few_kernel, dim3((unsigned)T, (unsigned)splits), dim3(FEW_THREADS), 0, st,
                 1, f);

@@ -57,8 +57,10 @@ __global__ void __launch_bounds__(THREADS)
   const uint32_t sb = (saddr(smem_raw) + 1023u) & ~1023u;
   const int p_bytes = g.nc * CHUNK, st_bytes = BIG_BYTES + 3 * p_bytes;
   volatile int* abort_flag = &s_abort;
-  uint32_t tcols = 32;
-  while ((int)tcols < 2 * g.n_mma) tcols *= 2;
+  // Two accumulators of 128 columns; for ranks up to 64 two pairs, taken in turn by the k steps
+  // (MMAs into one accumulator follow each other about 190 cycles apart however small they are)
+  const int pairs = g.nc == 1 ? 2 : 1;
+  const uint32_t tcols = tmem_columns(2 * pairs * g.n_mma);
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -139,10 +141,7 @@ __global__ void __launch_bounds__(THREADS)
     for (int s = 0; s < steps; ++s) {
       const int mine = ahead;
       if (s + 1 < steps) ahead = row_of(s + 1);
-      int w = 0;
-      if (lane == 0)
-        w = mbar_wait(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit);
-      if (!__shfl_sync(0xffffffffu, w, 0)) {
+      if (!mbar_wait_warp(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) {
         ok = false;
         break;
       }
@@ -201,35 +200,41 @@ __global__ void __launch_bounds__(THREADS)
         }
       }
     }
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------ MMA issuer
     // D fp32, A and B bf16, both MN-major (bits 15 and 16), M = 128, N = n_mma
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                            ((uint32_t)(g.n_mma >> 3) << 17) | (8u << 24);
+    const uint64_t bd0 = desc_sw128(sb, CHUNK, 1024), pd0 = desc_sw128(sb + BIG_BYTES, CHUNK, 1024);
     int stage = 0;
     uint32_t phase = 0;
     for (int s = 0; s < steps; ++s) {
-      if (!mbar_wait(saddr(&full[stage]), phase, abort_flag, g.status, limit)) break;
+      if (!mbar_wait_warp(saddr(&full[stage]), phase, abort_flag, g.status, limit)) break;
       fence_proxy_async_smem();  // the gathered rows (cp.async) -> MMA reads
       tc_fence_after();
-      const uint32_t bs = sb + stage * st_bytes, ps = bs + BIG_BYTES;
+      if (elect_one()) {
+        const uint64_t so = (uint64_t)((stage * st_bytes) >> 4);
 #pragma unroll
-      for (int kk = 0; kk < OT / 16; ++kk)
-        for (int q = 0; q < 3; ++q) {
-          const uint64_t bd = desc_sw128(ps + q * p_bytes + kk * 2048, CHUNK, 1024);
+        for (int q = 0; q < 3; ++q)
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-            tc_mma<1>(tmem + (uint32_t)(m * g.n_mma),
-                      desc_sw128(bs + m * 2 * CHUNK + kk * 2048, CHUNK, 1024), bd, idesc,
-                      (s | kk | q) != 0 ? 1u : 0u);
-        }
-      tc_commit<1>(saddr(&empty[stage]));
+          for (int kk = 0; kk < OT / 16; ++kk)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const int acc = 2 * (kk & (pairs - 1)) + m;
+              tc_mma<1>(tmem + (uint32_t)(acc * g.n_mma),
+                        bd0 + so + (uint64_t)((m * 2 * CHUNK + kk * 2048) >> 4),
+                        pd0 + so + (uint64_t)((q * p_bytes + kk * 2048) >> 4), idesc,
+                        (s > 0 || q > 0 || kk >= pairs) ? 1u : 0u);
+            }
+        tc_commit<1>(saddr(&empty[stage]));
+      }
+      __syncwarp();
       if (++stage == STAGES) {
         stage = 0;
         phase ^= 1u;
       }
     }
-    tc_commit<1>(saddr(&done));
+    if (elect_one()) tc_commit<1>(saddr(&done));
   }
   __syncwarp();
   int w_ok = 0;
@@ -248,26 +253,26 @@ __global__ void __launch_bounds__(THREADS)
       const int c = c0 + m * 128 + warp * 32 + lane;
 #pragma unroll 1
       for (int j0 = 0; j0 < g.r; j0 += 8) {
-        uint32_t v[8];
-        if (steps > 0) {
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-              : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
-                "=r"(v[6]), "=r"(v[7])
-              : "r"(tmem + (uint32_t)(m * g.n_mma + j0) + ((uint32_t)(warp * 32) << 16)));
-          tmem_ld_wait();
-        } else {
+        float f[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = 0u;
-        }
+        for (int j = 0; j < 8; ++j) f[j] = 0.f;
+        if (steps > 0)
+          for (int h = 0; h < pairs; ++h) {
+            uint32_t v[8];
+            tmem_ld8(tmem + (uint32_t)((2 * h + m) * g.n_mma + j0) +
+                         ((uint32_t)(warp * 32) << 16), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] += __uint_as_float(v[j]);
+          }
         if (c >= D || !ok) continue;
         if (p == 0) {
-          uint4* o = reinterpret_cast<uint4*>(dst + (size_t)c * g.r + j0);
-          o[0] = make_uint4(v[0], v[1], v[2], v[3]);
-          o[1] = make_uint4(v[4], v[5], v[6], v[7]);
+          float4* o = reinterpret_cast<float4*>(dst + (size_t)c * g.r + j0);
+          o[0] = make_float4(f[0], f[1], f[2], f[3]);
+          o[1] = make_float4(f[4], f[5], f[6], f[7]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dst[(size_t)(j0 + j) * D + c] = __uint_as_float(v[j]);
+          for (int j = 0; j < 8; ++j) dst[(size_t)(j0 + j) * D + c] = f[j];
         }
       }
     }

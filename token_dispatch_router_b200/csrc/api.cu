@@ -143,8 +143,8 @@ const char* kKernelNames[K_COUNT] = {
     "route_tc",     "permute_small", "gateup_tc2",   "down_tc2",
     "permute_cluster", "tile_round", "bwd_act", "bwd_dw", "bwd_dx",
     "router_dlogits", "router_dwr", "router_dx", "omni_logits", "omni_topk", "omni_count",
-    "omni_scan", "omni_scatter", "omni_sort", "omni_act", "omni_out", "decode_route", "decode",
-    "adapter_few",  "adapter_low_few", "adapter_low", "adapter_gemm", "adapter_outer",
+    "omni_scan", "omni_scatter", "omni_sort", "omni_act", "omni_out", "few_route", "few_up",
+    "few_down", "adapter_few",  "adapter_low_few", "adapter_low", "adapter_gemm", "adapter_outer",
     "adapter_outer_sum"};
 
 struct ProfRec {

@@ -1,48 +1,59 @@
-// Arguments of the few-token product kernel (few.cu), shared by the decode layer and the
-// adapter projection, and the layout of its control words.
+// What the kernels for a few tokens share: the size limit, the token masks of the experts, and
+// the small wrappers that they have in common.
 #pragma once
 
-#include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
-constexpr int kFewMaxTokens = 128;  // tokens on the MMA's N: two accumulators, double-buffered
-constexpr int kFewMaxSplit = 16;
-constexpr int kFewTarget = 1024;     // at most this many tiles are split over their contraction
+constexpr int kFewMaxTokens = 128;  // one 128-lane MMA tile of tokens
 constexpr int kFewMaxExperts = 256;
 
-// Control words, zero when the kernel starts: the kernel that runs before it in the same call
-// clears them.
-constexpr int kFewTicket = 0;                            // next unit of work
-constexpr int kFewDone = 1;                              // finished second-product units
-constexpr int kFewExpert = 2;                            // + active expert: finished act tiles
-constexpr int kFewTile = kFewExpert + kFewMaxExperts;    // + tile: arrived contraction splits
-constexpr int kFewCtlWords = kFewTile + kFewTarget;
-
-struct FewArgs {
-  int T, K, E;
-  int kb1, kb2;    // 64-wide k-blocks of the first and of the second product
-  int n, nt1;      // width of the first product's output, its 128-column tiles
-  int d, nt2;      // width of the second product's output, its 256-column tiles
-  int smax1, smax2;  // contraction splits that the partial buffers have room for
-  int cap;         // kept tokens per expert
-  int npad;        // T rounded up to 16: the MMA's N
-  int stages, stage_bytes;
-  const int32_t* ids;   // [T, K] (layer), or [T] (projection: the adapter of each token)
-  const float* topk_w;  // [T, K]
-  uint32_t* ctl;
-  bf16* act;     // [T * K, n]
-  float* part1;  // [T * K][nt1][split][256]
-  float* y32;    // [split][T * K][d]
-  bf16* out;     // [T, d]
-  // projection only
-  const float* low_part;  // [low_splits][T][rank]
-  float* low;             // [T, rank]
-  const bf16* b;          // [n_adapters, rank, d]
-  const float* scale;     // [n_adapters]
-  int rank, low_splits, n_adapters;
-  unsigned* status;
-  unsigned long long limit_ns;
+// Which tokens each expert keeps, and which experts have any.
+struct FewMasks {
+  unsigned mask[kFewMaxExperts][4];  // bit t of an expert's 128: token t is routed to it and kept
+  short act[kFewMaxExperts];         // the experts with a kept token, ascending
+  int n_act;
+  unsigned bad[4];                   // tokens with an id that is no expert (NaN logits)
 };
 
+// Called by every thread of the block (blockDim.x = n_threads); the masks are complete for all
+// of them when it returns. Over the capacity the first `cap` tokens of an expert stay.
+__device__ __forceinline__ void few_build_masks(FewMasks& m, const int32_t* ids, int T, int K,
+                                                int E, int cap, int n_threads) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int i = tid; i < 4 * E; i += n_threads) (&m.mask[0][0])[i] = 0u;
+  if (tid < 4) m.bad[tid] = 0u;
+  __syncthreads();
+  for (int a = tid; a < T * K; a += n_threads) {
+    const int e = ids[a], t = a / K;
+    if (e >= 0 && e < E) atomicOr(&m.mask[e][t >> 5], 1u << (t & 31));
+    else atomicOr(&m.bad[t >> 5], 1u << (t & 31));
+  }
+  __syncthreads();
+  if (tid < 32) {
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      int c = 0;
+      if (e < E) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          unsigned b = m.mask[e][w];
+          while (c + __popc(b) > cap) b &= ~(0x80000000u >> __clz(b));
+          m.mask[e][w] = b;
+          c += __popc(b);
+        }
+      }
+      const unsigned has = __ballot_sync(0xffffffffu, c > 0);
+      if (c > 0) m.act[n + __popc(has & lanemask_lt())] = (short)e;
+      n += __popc(has);
+    }
+    if (lane == 0) m.n_act = n;
+  }
+  __syncthreads();
+}
+
+// Four epilogue warps (barrier 1).
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 }  // namespace moe

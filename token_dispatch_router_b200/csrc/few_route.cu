@@ -149,10 +149,10 @@ moe_status run(const FewRouteArgs& a, cudaStream_t st) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
-  launch_begin(K_DECODE_ROUTE, st);
+  launch_begin(K_FEW_ROUTE, st);
   launch_kernel(kern, dim3((unsigned)((a.T + TG - 1) / TG * RANKS)), dim3(THREADS), smem, st,
                 RANKS, a);
-  return launch_end(K_DECODE_ROUTE, st);
+  return launch_end(K_FEW_ROUTE, st);
 }
 
 template <int TG>

@@ -37,8 +37,9 @@ enum KernelId {
   K_OMNI_SORT,
   K_OMNI_ACT,
   K_OMNI_OUT,
-  K_DECODE_ROUTE,
-  K_DECODE,
+  K_FEW_ROUTE,
+  K_FEW_UP,
+  K_FEW_DOWN,
   K_ADAPTER_FEW,
   K_ADAPTER_LOW_FEW,
   K_ADAPTER_LOW,
