@@ -1,6 +1,6 @@
 // Host side of the adapter products: workspace layouts and launch sequences.
 //
-//   forward,  at most 128 rows: low partials -> the few-token second product (two launches)
+//   forward,  at most 128 rows: low partials -> product with the adapter term (two launches)
 //   forward,  more rows:        group rows by adapter -> low -> product with the adapter term
 //   backward:                   group -> d_low -> d_x product with the adapter term
 //                               -> outer products d_A, d_B
@@ -16,7 +16,7 @@ size_t permute_scratch_bytes(const moe_shape& s);
 moe_status launch_permute(const moe_shape& s, const int32_t* ids, int32_t* counts,
                           int32_t* offsets, int32_t* a2p, int32_t* p2a, const void* x,
                           void* x_perm, void* scratch, cudaStream_t st);
-moe_status launch_adapter_few(FewDownArgs a, int d_in, const void* x, const void* w,
+moe_status launch_adapter_few(const AdapterFewArgs& a, int d_in, const void* x, const void* w,
                               cudaStream_t st);
 moe_status launch_adapter_low_few(int T, int D, int r, int L, int splits, const void* x,
                                   const void* a, const int32_t* ids, float* part,
@@ -108,11 +108,8 @@ moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, con
                                   cudaStream_t st) {
   moe_status r;
   if (s.T <= kFewMaxTokens) {
-    FewDownArgs f = {};
+    AdapterFewArgs f = {};
     f.T = s.T;
-    f.K = 1;
-    f.E = 1;
-    f.cap = s.T;
     f.d = s.d_out;
     f.ids = ids;
     f.out = (bf16*)y;

@@ -54,6 +54,18 @@ __device__ __forceinline__ void few_build_masks(FewMasks& m, const int32_t* ids,
   __syncthreads();
 }
 
+// A line of `total` blocks cut into equal pieces, one per CTA: how many pieces (each of `least`
+// blocks or more), where piece c begins, and the piece that holds block b.
+__device__ __forceinline__ int few_pieces(long long total, int least, int ctas) {
+  return (int)max(1LL, min((long long)ctas, total / least));
+}
+__device__ __forceinline__ long long few_piece_begin(long long c, long long total, int pieces) {
+  return c * total / pieces;
+}
+__device__ __forceinline__ int few_piece_of(long long b, long long total, int pieces) {
+  return (int)(((b + 1) * pieces - 1) / total);
+}
+
 // Four epilogue warps (barrier 1).
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 }  // namespace moe

@@ -1,4 +1,4 @@
-// Arguments of the two product kernels for a few tokens.
+// Arguments of the product kernels for a few tokens.
 #pragma once
 
 #include "common.cuh"
@@ -19,19 +19,29 @@ struct FewUpArgs {
 };
 
 struct FewDownArgs {
-  int T, K, E, cap;
-  int kb;      // 64-wide k-blocks of one expert's matrix, or of the projection
-  int d;       // output width
-  const int32_t* ids;  // [T, K] (layer), or [T]: the adapter of each row (projection)
+  int T, K, E, cap, n, d;
+  const int32_t* ids;  // [T, K]
   bf16* out;           // [T, d]
-  // projection only
-  const float* low_part;  // [low_splits][T][rank]
-  float* low;             // [T, rank]
-  const bf16* b;          // [n_adapters, rank, d]
-  const float* scale;     // [n_adapters]
-  int rank, low_splits, n_adapters;
+  float* part;         // [2 pieces][32][T][4]: partials of cut tiles
+  uint32_t* arrived;   // [pieces], zero when the kernel starts
   // set by the launcher
-  int split, stages, stage_bytes, ring_bytes;
+  int kb, nt;  // stages of one expert's matrix; 128-column tiles
+  int stages, stage_bytes;
+  unsigned* status;
+  unsigned long long limit_ns;
+};
+
+struct AdapterFewArgs {
+  int T, d;                // d: output width
+  const int32_t* ids;      // [T]
+  const float* low_part;   // [low_splits][T][rank]
+  float* low;              // [T, rank]
+  const bf16* b;           // [n_adapters, rank, d]
+  const float* scale;      // [n_adapters]
+  int rank, low_splits, n_adapters;
+  bf16* out;               // [T, d]
+  // set by the launcher
+  int kb, split, stages, stage_bytes, ring_bytes;
   unsigned* status;
   unsigned long long limit_ns;
 };

@@ -14,8 +14,10 @@
 // per SM: every SM reads the same number of bytes whatever the number of experts and tiles. A
 // tile cut by a piece's end leaves fp32 partials, which the last of its SMs to finish adds in
 // the line's order (nobody waits; results repeat bit for bit).
-// Roles (192 threads): warp 0 loads, warp 1 issues the MMAs (two accumulators, double-buffered),
-// warps 2-5 read them (lane = weight column, column = token). Every wait is bounded; on expiry
+// Roles (256 threads): warp 0 copies the weights, warp 2 the rows of x (a copy takes its warp
+// about 60 cycles to issue, a finished wait 200: one warp for both was the bound), warp 1 issues
+// the MMAs (two accumulators, double-buffered), warps 4-7 read them (lane = weight column, column
+// = token). Every wait is bounded; on expiry
 // the status word records MOE_ERR_TIMEOUT and the CTA ends after its copies and MMAs in flight.
 #include "few.cuh"
 #include "few_args.cuh"
@@ -27,7 +29,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int THREADS = 192;
+constexpr int THREADS = 256;
 constexpr int BK = 64;
 constexpr int W_CHUNK = 8192;         // 64 k-rows x 64 columns
 constexpr int W_BYTES = 4 * W_CHUNK;  // 128 columns of W_gate and of W_up
@@ -37,26 +39,13 @@ constexpr int MIN_BLOCKS = 4;         // k-blocks of a piece, at least
 constexpr int SMEM_LIMIT = 227 * 1024;
 
 struct Tail {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], done;
+  uint64_t full[MAX_STAGES], full_x[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], done;
   uint32_t tmem;
   int abort, epi_ok, last;
   FewMasks m;
   float w[kFewMaxTokens];         // the unit's expert: its tokens' routing weights
   unsigned char tok[kFewMaxTokens];  // and the tokens, ascending
 };
-
-struct Piece {
-  long long begin, end;  // k-blocks of the line
-  int pieces;            // CTAs with work
-  long long total;
-};
-__device__ __forceinline__ long long piece_begin(long long c, long long total, int pieces) {
-  return c * total / pieces;
-}
-// The piece that holds k-block b.
-__device__ __forceinline__ int piece_of(long long b, long long total, int pieces) {
-  return (int)(((b + 1) * pieces - 1) / total);
-}
 
 __device__ __forceinline__ int count_of(const unsigned (&m)[4]) {
   return __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
@@ -92,6 +81,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (tid == 0) {
     for (int s = 0; s < g.stages; ++s) {
       mbar_init(saddr(&t.full[s]), 1);
+      mbar_init(saddr(&t.full_x[s]), 1);
       mbar_init(saddr(&t.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -112,14 +102,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = t.tmem;
   const uint64_t limit = g.limit_ns;
   const long long total = (long long)t.m.n_act * g.nt * g.kblocks;
-  const int pieces = (int)max(1LL, min((long long)gridDim.x, total / MIN_BLOCKS));
+  const int pieces = few_pieces(total, MIN_BLOCKS, (int)gridDim.x);
   const bool work = (int)blockIdx.x < pieces && total > 0;
-  const long long b0 = work ? piece_begin(blockIdx.x, total, pieces) : 0;
-  const long long b1 = work ? piece_begin(blockIdx.x + 1, total, pieces) : 0;
+  const long long b0 = work ? few_piece_begin(blockIdx.x, total, pieces) : 0;
+  const long long b1 = work ? few_piece_begin(blockIdx.x + 1, total, pieces) : 0;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ loads
-    // lane i copies four of the expert's tokens, lanes 0-3 also a piece of the weights each
+    // warp 0: a copy each of W_gate and W_up; warp 2: lane i four of the expert's tokens
+    const bool x_warp = warp == 2;
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_par = 0;
     int k = (int)(b0 % g.kblocks), ct = (int)(b0 / g.kblocks) % g.nt;
@@ -129,19 +120,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       e = t.m.act[a];
       const int n = count_of(t.m.mask[e]);
       quads = (n + 15) / 16 * 4;
+      if (x_warp)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) row[i] = token_at(t.m.mask[e], 4 * lane + i < n ? 4 * lane + i : 0);
+        for (int i = 0; i < 4; ++i)
+          row[i] = token_at(t.m.mask[e], 4 * lane + i < n ? 4 * lane + i : 0);
     };
     if (work) enter();
     for (long long b = b0; b < b1; ++b) {
       if (!mbar_wait_warp(saddr(&t.empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
-      const uint32_t fb = saddr(&t.full[stage]), w = saddr(base + stage * g.stage_bytes);
-      if (lane == 0) mbar_expect_tx(fb, (uint32_t)(W_BYTES + quads * X_BOX));
+      const uint32_t fb = saddr(x_warp ? &t.full_x[stage] : &t.full[stage]);
+      const uint32_t w = saddr(base + stage * g.stage_bytes);
+      if (x_warp) {
+        if (lane == 0) mbar_expect_tx(fb, (uint32_t)(quads * X_BOX));
+        __syncwarp();
+        if (lane < quads) tma_gather4(w + W_BYTES + lane * X_BOX, &tmX, k * BK, row, fb);
+      } else if (elect_one()) {
+        mbar_expect_tx(fb, W_BYTES);
+        tma_load_4d(w, &tmG, 0, k * BK, ct * 2, e, fb);
+        tma_load_4d(w + 2 * W_CHUNK, &tmU, 0, k * BK, ct * 2, e, fb);
+      }
       __syncwarp();
-      if (lane < 4)
-        tma_load_3d(w + lane * W_CHUNK, lane < 2 ? &tmG : &tmU, ct * 128 + (lane & 1) * 64, k * BK,
-                    e, fb);
-      if (lane < quads) tma_gather4(w + W_BYTES + lane * X_BOX, &tmX, k * BK, row, fb);
       issued_mask |= 1u << stage;
       issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
       if (++stage == g.stages) {
@@ -160,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int s = 0; s < g.stages; ++s) {  // nothing of ours is in flight after this (bounded)
         if (!(issued_mask & (1u << s))) continue;
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try(saddr(&t.full[s]), (issued_par >> s) & 1u) &&
+        while (!mbar_try(saddr(x_warp ? &t.full_x[s] : &t.full[s]), (issued_par >> s) & 1u) &&
                globaltimer_ns() - t0 < limit) {
         }
       }
@@ -185,7 +183,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)(buf * 2 * g.npad);
       for (bool first = true; b < stop; ++b, first = false) {
-        if (!mbar_wait_warp(saddr(&t.full[stage]), phase, abort_flag, g.status, limit)) {
+        if (!mbar_wait_warp(saddr(&t.full[stage]), phase, abort_flag, g.status, limit) ||
+            !mbar_wait_warp(saddr(&t.full_x[stage]), phase, abort_flag, g.status, limit)) {
           ok = false;
           break;
         }
@@ -217,10 +216,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       while (!mbar_try(saddr(&t.done), 0) && globaltimer_ns() - t0 < limit) {
       }
     }
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     // One thread waits for all four warps, so that they leave a wait that ran out together.
-    const int et = tid - 64, q = warp & 3;  // TMEM lanes 32 q ...
+    const int et = tid - 128, q = warp & 3;  // TMEM lanes 32 q ...
     const bool first = et == 0;
     const int cl = q * 32 + lane;
     int it = 0, last_e = -1;
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(saddr(&t.tempty[buf]));
       if (!whole) {
-        const int p0 = piece_of(tile0, total, pieces), p1 = piece_of(tile1 - 1, total, pieces);
+        const int p0 = few_piece_of(tile0, total, pieces), p1 = few_piece_of(tile1 - 1, total, pieces);
         __threadfence();
         epi_bar();
         if (first) t.last = atomicAdd(g.arrived + p0, 1u) == (unsigned)(p1 - p0);
@@ -295,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             float gf = 0.f, uf = 0.f;
 #pragma unroll 4
             for (int p = p0; p <= p1; ++p) {
-              const int s = 2 * p + (tile0 >= piece_begin(p, total, pieces) ? 1 : 0);
+              const int s = 2 * p + (tile0 >= few_piece_begin(p, total, pieces) ? 1 : 0);
               const float* pp = g.part + ((size_t)s * g.T + j) * 256 + cl;
               gf += __ldcg(pp);
               uf += __ldcg(pp + 128);
@@ -331,12 +330,10 @@ moe_status launch_few_up(FewUpArgs a, int d, int n_experts, const void* x, const
   a.status = device_status_ptr();
   a.limit_ns = kWaitLimitNs;
   CUtensorMap mx, mg, mu;
-  const uint64_t k = d, n = a.n, E = n_experts;
-  const uint32_t wbox[3] = {64, 64, 1}, xbox[2] = {64, 1};
-  const uint64_t wd[3] = {n, k, E}, ws[2] = {n * 2, k * n * 2};
-  const uint64_t xd[2] = {k, (uint64_t)a.T}, xs[1] = {k * 2};
-  if (!make_map(&mx, x, 2, xd, xs, xbox) || !make_map(&mg, w_gate, 3, wd, ws, wbox) ||
-      !make_map(&mu, w_up, 3, wd, ws, wbox))
+  const uint64_t xd[2] = {(uint64_t)d, (uint64_t)a.T}, xs[1] = {(uint64_t)d * 2};
+  const uint32_t xbox[2] = {64, 1};
+  if (!make_map(&mx, x, 2, xd, xs, xbox) || !make_piece_map(&mg, w_gate, d, a.n, n_experts, BK, 2) ||
+      !make_piece_map(&mu, w_up, d, a.n, n_experts, BK, 2))
     return MOE_ERR_CUDA;
   if (cudaFuncSetAttribute(few_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            SMEM_LIMIT) != cudaSuccess)
