@@ -16,12 +16,6 @@ struct AdapterTile {
   uint32_t off[kAdapterTileRows][8];
 };
 
-// 16 bytes global -> shared, zeros when `on` is false (nothing is read then).
-__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(on ? 16 : 0)
-               : "memory");
-}
 // (a, b) as bf16 pairs hi + lo (+ what is left, returned in a and b): 8 bits of mantissa each.
 __device__ __forceinline__ uint32_t take_bf16x2(float& a, float& b) {
   const uint32_t h = pack_bf16x2(a, b);

@@ -1,5 +1,5 @@
-// Host side of the few-token layer: workspace layout and the three launches (router, first
-// expert product, second expert product with the sum over experts).
+// Host side of the few-token layer: workspace layout and the launches (router, first
+// expert product, second expert product with the sum over experts, partial sums of cut tiles).
 #include "few.cuh"
 #include "few_args.cuh"
 
@@ -13,8 +13,7 @@ size_t few_up_part_bytes(int T);
 moe_status launch_few_up(FewUpArgs a, int d, int n_experts, const void* x, const void* w_gate,
                          const void* w_up, cudaStream_t st);
 size_t few_down_part_bytes(int T);
-moe_status launch_few_down(FewDownArgs a, int active, const void* act, const void* w_down,
-                           cudaStream_t st);
+moe_status launch_few_down(FewDownArgs a, const void* w_down, cudaStream_t st);
 
 namespace {
 
@@ -32,7 +31,7 @@ Layout layout(const moe_shape& s) {
   };
   const size_t A = (size_t)s.T * s.K;
   L.active = A < (size_t)s.E ? (int)A : s.E;
-  L.arrived = take((size_t)2 * few_up_pieces() * 4);  // few_up's, few_down's
+  L.arrived = take((size_t)few_up_pieces() * 4);
   L.ids = take(A * 4);
   L.w = take(A * 4);
   L.act = take((size_t)L.active * s.T * s.n * 2);
@@ -71,17 +70,17 @@ moe_status launch_decode(const moe_shape& s, const void* x, const void* w_r, con
   dn.cap = cap;
   dn.n = s.n;
   dn.d = s.d;
+  dn.act = u.act;
   dn.part = u.part;
-  dn.arrived = u.arrived + few_up_pieces();
   dn.ids = ids;
   dn.out = (bf16*)out;
   moe_status r;
   if ((r = launch_few_route(s, x, w_r, bias, logits_in, ids, w, u.arrived,
-                            2 * few_up_pieces(), st)) !=
+                            few_up_pieces(), st)) !=
       MOE_OK)
     return r;
   if ((r = launch_few_up(u, s.d, s.E, x, w_gate, w_up, st)) != MOE_OK) return r;
-  return launch_few_down(dn, L.active, u.act, w_down, st);
+  return launch_few_down(dn, w_down, st);
 }
 
 }  // namespace moe

@@ -54,6 +54,9 @@ __device__ __forceinline__ void few_build_masks(FewMasks& m, const int32_t* ids,
   __syncthreads();
 }
 
+__device__ __forceinline__ int few_count(const unsigned (&m)[4]) {
+  return __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
+}
 // A line of `total` blocks cut into equal pieces, one per CTA: how many pieces (each of `least`
 // blocks or more), where piece c begins, and the piece that holds block b.
 __device__ __forceinline__ int few_pieces(long long total, int least, int ctas) {

@@ -21,12 +21,12 @@ struct FewUpArgs {
 struct FewDownArgs {
   int T, K, E, cap, n, d;
   const int32_t* ids;  // [T, K]
+  const bf16* act;     // [active experts][T][n]
   bf16* out;           // [T, d]
   float* part;         // [2 pieces][32][T][4]: partials of cut tiles
-  uint32_t* arrived;   // [pieces], zero when the kernel starts
   // set by the launcher
   int kb, nt;  // stages of one expert's matrix; 128-column tiles
-  int stages, stage_bytes;
+  int stages, x_stages, ring_bytes;
   unsigned* status;
   unsigned long long limit_ns;
 };

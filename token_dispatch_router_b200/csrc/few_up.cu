@@ -47,9 +47,6 @@ struct Tail {
   unsigned char tok[kFewMaxTokens];  // and the tokens, ascending
 };
 
-__device__ __forceinline__ int count_of(const unsigned (&m)[4]) {
-  return __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
-}
 // The j-th token of a mask (j below its count).
 __device__ __forceinline__ int token_at(const unsigned (&m)[4], int j) {
 #pragma unroll
@@ -111,6 +108,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ loads
     // warp 0: a copy each of W_gate and W_up; warp 2: lane i four of the expert's tokens
     const bool x_warp = warp == 2;
+    const uint64_t once = l2_policy_evict_first();  // weights are read once: x and act stay in L2
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_par = 0;
     int k = (int)(b0 % g.kblocks), ct = (int)(b0 / g.kblocks) % g.nt;
@@ -118,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int row[4] = {0, 0, 0, 0};
     auto enter = [&]() {  // the rows behind the last token repeat the first one
       e = t.m.act[a];
-      const int n = count_of(t.m.mask[e]);
+      const int n = few_count(t.m.mask[e]);
       quads = (n + 15) / 16 * 4;
       if (x_warp)
 #pragma unroll
@@ -136,8 +134,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane < quads) tma_gather4(w + W_BYTES + lane * X_BOX, &tmX, k * BK, row, fb);
       } else if (elect_one()) {
         mbar_expect_tx(fb, W_BYTES);
-        tma_load_4d(w, &tmG, 0, k * BK, ct * 2, e, fb);
-        tma_load_4d(w + 2 * W_CHUNK, &tmU, 0, k * BK, ct * 2, e, fb);
+        tma_load_4d_hint(w, &tmG, 0, k * BK, ct * 2, e, fb, once);
+        tma_load_4d_hint(w + 2 * W_CHUNK, &tmU, 0, k * BK, ct * 2, e, fb, once);
       }
       __syncwarp();
       issued_mask |= 1u << stage;
@@ -174,7 +172,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (long long b = b0; b < b1 && ok; ++it) {
       const long long stop = min(b1, (b / g.kblocks + 1) * g.kblocks);
-      const int n_tok = count_of(t.m.mask[t.m.act[(int)(b / g.kblocks) / g.nt]]);
+      const int n_tok = few_count(t.m.mask[t.m.act[(int)(b / g.kblocks) / g.nt]]);
       const uint32_t idesc = idesc0 | ((uint32_t)((n_tok + 15) / 16 * 2) << 17);
       const int buf = it & 1;
       if (!mbar_wait_warp(saddr(&t.tempty[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag,
@@ -260,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // most two, the tile that it begins in and the tile that begins in it
       const int slot = 2 * (int)blockIdx.x + (tile0 >= b0 ? 1 : 0);
       float* part = g.part + (size_t)slot * g.T * 256 + cl;
-      const int n_tok = count_of(t.m.mask[e]);
+      const int n_tok = few_count(t.m.mask[e]);
       for (int j0 = 0; j0 < n_tok; j0 += 8) {
         uint32_t gv[8], uv[8];
         tmem_ld8(acc + (uint32_t)j0, gv);

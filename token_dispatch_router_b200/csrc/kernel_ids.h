@@ -40,6 +40,7 @@ enum KernelId {
   K_FEW_ROUTE,
   K_FEW_UP,
   K_FEW_DOWN,
+  K_FEW_SUM,
   K_ADAPTER_FEW,
   K_ADAPTER_LOW_FEW,
   K_ADAPTER_LOW,
