@@ -13,7 +13,7 @@ constexpr int kFewMaxExperts = 256;
 struct FewMasks {
   unsigned mask[kFewMaxExperts][4];  // bit t of an expert's 128: token t is routed to it and kept
   short act[kFewMaxExperts];         // the experts with a kept token, ascending
-  int n_act;
+  int n_act, most;                   // how many, and the most tokens of one
   unsigned bad[4];                   // tokens with an id that is no expert (NaN logits)
 };
 
@@ -32,7 +32,7 @@ __device__ __forceinline__ void few_build_masks(FewMasks& m, const int32_t* ids,
   }
   __syncthreads();
   if (tid < 32) {
-    int n = 0;
+    int n = 0, most = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
       int c = 0;
@@ -48,8 +48,13 @@ __device__ __forceinline__ void few_build_masks(FewMasks& m, const int32_t* ids,
       const unsigned has = __ballot_sync(0xffffffffu, c > 0);
       if (c > 0) m.act[n + __popc(has & lanemask_lt())] = (short)e;
       n += __popc(has);
+      most = max(most, c);
     }
-    if (lane == 0) m.n_act = n;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      m.n_act = n;
+      m.most = most;
+    }
   }
   __syncthreads();
 }

@@ -23,10 +23,10 @@ struct FewDownArgs {
   const int32_t* ids;  // [T, K]
   const bf16* act;     // [active experts][T][n]
   bf16* out;           // [T, d]
-  float* part;         // [2 pieces][32][T][4]: partials of cut tiles
+  float* part;         // [2 pieces][T][128]: partials of cut tiles
   // set by the launcher
   int kb, nt;  // stages of one expert's matrix; 128-column tiles
-  int stages, x_stages, ring_bytes;
+  int ring_bytes;
   unsigned* status;
   unsigned long long limit_ns;
 };
