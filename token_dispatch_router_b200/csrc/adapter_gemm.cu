@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) mbar_arrive_remote(tempty_leader + (uint32_t)(buf * 8));
     }
   }
+  __syncwarp();  // lanes that waited alone are back: a barrier counts a split warp twice
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the pair is done with both TMEM allocations and all barriers

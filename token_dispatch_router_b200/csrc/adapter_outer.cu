@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 4) {

@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tile_b = b;
     }
   }
+  __syncwarp();  // lanes that waited alone are back: a barrier counts a split warp twice
   tc_fence_before();
   __syncthreads();
   if (warp == 2) {

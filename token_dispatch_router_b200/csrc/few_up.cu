@@ -288,22 +288,33 @@ __global__ void __launch_bounds__(THREADS, 1)
         epi_bar();
         if (t.last) {
           __threadfence();
-          for (int j = 0; j < n_tok; ++j) {
-            float gf = 0.f, uf = 0.f;
-#pragma unroll 4
+          // eight tokens at a time, so that their loads are in flight together
+          for (int j0 = 0; j0 < n_tok; j0 += 8) {
+            float gf[8], uf[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) gf[i] = uf[i] = 0.f;
             for (int p = p0; p <= p1; ++p) {
               const int s = 2 * p + (tile0 >= few_piece_begin(p, total, pieces) ? 1 : 0);
-              const float* pp = g.part + ((size_t)s * g.T + j) * 256 + cl;
-              gf += __ldcg(pp);
-              uf += __ldcg(pp + 128);
+              const float* pp = g.part + ((size_t)s * g.T + j0) * 256 + cl;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (j0 + i < n_tok) {
+                  gf[i] += __ldcg(pp + i * 256);
+                  uf[i] += __ldcg(pp + i * 256 + 128);
+                }
             }
-            if (col_ok) act[(size_t)t.tok[j] * g.n] = __float2bfloat16(t.w[j] * silu_mul(gf, uf));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (j0 + i < n_tok && col_ok)
+                act[(size_t)t.tok[j0 + i] * g.n] =
+                    __float2bfloat16(t.w[j0 + i] * silu_mul(gf[i], uf[i]));
           }
         }
       }
       b = stop;
     }
   }
+  __syncwarp();  // lanes that waited alone are back: a barrier counts a split warp twice
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
