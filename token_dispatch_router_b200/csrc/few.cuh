@@ -17,14 +17,17 @@ struct FewMasks {
   unsigned bad[4];                   // tokens with an id that is no expert (NaN logits)
 };
 
-// Called by every thread of the block (blockDim.x = n_threads); the masks are complete for all
-// of them when it returns. Over the capacity the first `cap` tokens of an expert stay.
+// few_clear_masks, then few_build_masks, by every thread of the block (n_threads): the masks are
+// complete for all of them when the second returns. Over the capacity the first `cap` tokens of
+// an expert stay. Clearing needs no global memory, so it can come before a wait.
+__device__ __forceinline__ void few_clear_masks(FewMasks& m, int E, int n_threads) {
+  for (int i = threadIdx.x; i < 4 * E; i += n_threads) (&m.mask[0][0])[i] = 0u;
+  if (threadIdx.x < 4) m.bad[threadIdx.x] = 0u;
+  __syncthreads();
+}
 __device__ __forceinline__ void few_build_masks(FewMasks& m, const int32_t* ids, int T, int K,
                                                 int E, int cap, int n_threads) {
   const int tid = threadIdx.x, lane = tid & 31;
-  for (int i = tid; i < 4 * E; i += n_threads) (&m.mask[0][0])[i] = 0u;
-  if (tid < 4) m.bad[tid] = 0u;
-  __syncthreads();
   for (int a = tid; a < T * K; a += n_threads) {
     const int e = ids[a], t = a / K;
     if (e >= 0 && e < E) atomicOr(&m.mask[e][t >> 5], 1u << (t & 31));
@@ -62,17 +65,21 @@ __device__ __forceinline__ void few_build_masks(FewMasks& m, const int32_t* ids,
 __device__ __forceinline__ int few_count(const unsigned (&m)[4]) {
   return __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
 }
-// A line of `total` blocks cut into equal pieces, one per CTA: how many pieces (each of `least`
-// blocks or more), where piece c begins, and the piece that holds block b.
-__device__ __forceinline__ int few_pieces(long long total, int least, int ctas) {
-  return (int)max(1LL, min((long long)ctas, total / least));
-}
-__device__ __forceinline__ long long few_piece_begin(long long c, long long total, int pieces) {
-  return c * total / pieces;
-}
-__device__ __forceinline__ int few_piece_of(long long b, long long total, int pieces) {
-  return (int)(((b + 1) * pieces - 1) / total);
-}
+// A line of `total` blocks cut into equal pieces, one per CTA, at least `least` blocks each (the
+// first ones a block longer): where piece c begins, and the piece that holds block b.
+struct FewPieces {
+  int n, q, r;
+  __device__ __forceinline__ FewPieces(int total, int least, int ctas) {
+    n = max(1, min(ctas, total / least));
+    q = total / n;
+    r = total - q * n;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int of(int b) const {
+    const int longer = r * (q + 1);
+    return b < longer ? b / (q + 1) : r + (b - longer) / q;
+  }
+};
 
 // Four epilogue warps (barrier 1).
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }

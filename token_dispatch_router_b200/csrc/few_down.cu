@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init_fence();
   }
   if (warp == 2) tmem_alloc<1>(saddr(&t.tmem), TMEM_COLS);
+  if (tid == 96) prefetch_map(&tmW);
+  few_clear_masks(t.m, g.E, THREADS);
   // ids: written by the kernel before the previous one, which is complete
   few_build_masks(t.m, g.ids, g.T, g.K, g.E, g.cap, THREADS);
   for (int i = tid; i < t.m.n_act; i += THREADS) {
@@ -107,20 +109,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t x_most = (uint32_t)(t.m.most + 15) / 16u * (16u * 128u);
   const uint32_t stage_bytes = W_BYTES + PIECES * x_most, ring = saddr(base);
   const int stages = min(MAX_STAGES, (int)((uint32_t)g.ring_bytes / stage_bytes));
-  const int line = t.m.n_act * g.kb;
-  const long long total = (long long)line * g.nt;
-  const int pieces = few_pieces(total, MIN_BLOCKS, (int)gridDim.x);
-  const bool work = (int)blockIdx.x < pieces && total > 0;
-  const long long b0 = work ? few_piece_begin(blockIdx.x, total, pieces) : 0;
-  const long long b1 = work ? few_piece_begin(blockIdx.x + 1, total, pieces) : 0;
-  const int at0 = line > 0 ? (int)(b0 % line) : 0;  // of the first block, in its tile's line
+  const int line = t.m.n_act * g.kb, total = line * g.nt;
+  const FewPieces cut(total, MIN_BLOCKS, (int)gridDim.x);
+  const bool work = (int)blockIdx.x < cut.n && total > 0;
+  const int b0 = work ? cut.begin(blockIdx.x) : 0, b1 = work ? cut.begin(blockIdx.x + 1) : 0;
+  const int at0 = line > 0 ? b0 % line : 0;  // of the first block, in its tile's line
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights
-    int tile = line > 0 ? (int)(b0 / line) : 0, a = at0 / g.kb, k = at0 % g.kb, stage = 0;
+    int tile = line > 0 ? b0 / line : 0, a = at0 / g.kb, k = at0 % g.kb, stage = 0;
     uint32_t phase = 0;
     const uint64_t once = l2_policy_evict_first();  // read once: act stays in L2
-    for (long long b = b0; b < b1; ++b) {
+    for (int b = b0; b < b1; ++b) {
       if (!mbar_wait_warp(saddr(&t.empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
       if (elect_one()) {
         const uint32_t fb = saddr(&t.full[stage]);
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     pdl_wait();  // act is complete
     int stage = 0;
     uint32_t phase = 0;
-    for (long long b = b0; b < b1; ++b) {
+    for (int b = b0; b < b1; ++b) {
       if (!mbar_wait_warp(saddr(&t.empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
       const uint32_t x = ring + (uint32_t)stage * stage_bytes + W_BYTES +
                          (uint32_t)(piece >> 3) * x_most;
@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     int stage = 0, it = 0, a = at0 / g.kb, k = at0 % g.kb;
     uint32_t phase = 0;
     bool ok = true;
-    for (long long b = b0; b < b1 && ok; ++it) {  // an expert's blocks at a time
-      const long long stop = min(b1, b + g.kb - k);
+    for (int b = b0; b < b1 && ok; ++it) {  // an expert's blocks at a time
+      const int stop = min(b1, b + g.kb - k);
       const int buf = it & 1, n_tok = few_count(t.m.mask[t.m.act[a]]);
       const uint32_t idesc = idesc0 | ((uint32_t)((n_tok + 15) / 16 * 2) << 17);
       if (!mbar_wait_warp(saddr(&t.tempty[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag,
@@ -243,9 +243,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     pdl_trigger();
     int it = 0, a = at0 / g.kb, k = at0 % g.kb;
     bool fresh = true;  // the tile has no sum yet
-    long long tile_b = b0;
-    for (long long b = b0; b < b1; ++it) {
-      const long long stop = min(b1, b + g.kb - k);
+    int tile_b = b0;
+    for (int b = b0; b < b1; ++it) {
+      const int stop = min(b1, b + g.kb - k);
       const int buf = it & 1, e = t.m.act[a], n_tok = few_count(t.m.mask[e]);
       const unsigned char* tok = t.tok + t.first[e];
       if (fresh) {
@@ -279,8 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (++a == t.m.n_act) a = 0;
       if (a != 0 && b < b1) continue;
       // ---- the tile's end, or the piece's
-      const int tile = (int)((b - 1) / line), col = tile * BN + cl;
-      const long long tile0 = (long long)tile * line;
+      const int tile = (b - 1) / line, col = tile * BN + cl, tile0 = tile * line;
       const bool whole = tile_b == tile0 && b == tile0 + line;
       // partials of a cut tile: [slot][token][128]; a piece has at most two, the tile that it
       // begins in and the tile that begins in it
@@ -317,25 +316,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 // columns of one token a thread. g as few_down_kernel had it, `ctas` its grid.
 __global__ void __launch_bounds__(THREADS) few_sum_kernel(const FewDownArgs g, int ctas) {
   __shared__ FewMasks m;
+  few_clear_masks(m, g.E, THREADS);
   few_build_masks(m, g.ids, g.T, g.K, g.E, g.cap, THREADS);  // complete before that kernel began
-  const int line = m.n_act * g.kb;
-  const long long total = (long long)line * g.nt;
-  const int pieces = few_pieces(total, MIN_BLOCKS, ctas);
+  const int line = m.n_act * g.kb, total = line * g.nt;
+  const FewPieces cut(total, MIN_BLOCKS, ctas);
   const int i = (int)blockIdx.x * THREADS + (int)threadIdx.x;
   const int c4 = i % (BN / 4) * 4, tok = i / (BN / 4) % g.T, tile = i / (BN / 4) / g.T;
   const int col = tile * BN + c4;
+  const int tile0 = tile * line, p0 = total > 0 && tile < g.nt ? cut.of(tile0) : 0;
+  const int p1 = total > 0 && tile < g.nt ? cut.of(tile0 + line - 1) : 0;
   pdl_wait();  // the previous kernel in the stream has completed
   pdl_trigger();
   if (tile >= g.nt || col >= g.d) return;
   float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
   if (total > 0) {
-    const long long tile0 = (long long)tile * line;
-    const int p0 = few_piece_of(tile0, total, pieces);
-    const int p1 = few_piece_of(tile0 + line - 1, total, pieces);
     if (p0 == p1) return;  // one piece held all of it and wrote it
 #pragma unroll 8
     for (int p = p0; p <= p1; ++p) {
-      const int s = 2 * p + (tile0 >= few_piece_begin(p, total, pieces) ? 1 : 0);
+      const int s = 2 * p + (tile0 >= cut.begin(p) ? 1 : 0);
       const float4 v =
           __ldcg(reinterpret_cast<const float4*>(g.part + ((size_t)s * g.T + tok) * BN + c4));
       f.x += v.x; f.y += v.y; f.z += v.z; f.w += v.w;

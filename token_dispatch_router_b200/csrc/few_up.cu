@@ -90,19 +90,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc<1>(saddr(&t.tmem), tcols);
+  if (tid == 64) {
+    prefetch_map(&tmX);
+    prefetch_map(&tmG);
+    prefetch_map(&tmU);
+  }
   tc_fence_before();
-  __syncthreads();
+  few_clear_masks(t.m, g.E, THREADS);  // a barrier for the whole block
   tc_fence_after();
   pdl_wait();  // the previous kernel in the stream has completed
   pdl_trigger();
   few_build_masks(t.m, g.ids, g.T, g.K, g.E, g.cap, THREADS);
   const uint32_t tmem = t.tmem;
   const uint64_t limit = g.limit_ns;
-  const long long total = (long long)t.m.n_act * g.nt * g.kblocks;
-  const int pieces = few_pieces(total, MIN_BLOCKS, (int)gridDim.x);
-  const bool work = (int)blockIdx.x < pieces && total > 0;
-  const long long b0 = work ? few_piece_begin(blockIdx.x, total, pieces) : 0;
-  const long long b1 = work ? few_piece_begin(blockIdx.x + 1, total, pieces) : 0;
+  const int total = t.m.n_act * g.nt * g.kblocks;
+  const FewPieces cut(total, MIN_BLOCKS, (int)gridDim.x);
+  const bool work = (int)blockIdx.x < cut.n && total > 0;
+  const int b0 = work ? cut.begin(blockIdx.x) : 0, b1 = work ? cut.begin(blockIdx.x + 1) : 0;
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ loads
@@ -111,8 +115,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint64_t once = l2_policy_evict_first();  // weights are read once: x and act stay in L2
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_par = 0;
-    int k = (int)(b0 % g.kblocks), ct = (int)(b0 / g.kblocks) % g.nt;
-    int a = (int)(b0 / g.kblocks) / g.nt, e = 0, quads = 0;
+    int k = b0 % g.kblocks, ct = b0 / g.kblocks % g.nt;
+    int a = b0 / g.kblocks / g.nt, e = 0, quads = 0;
     int row[4] = {0, 0, 0, 0};
     auto enter = [&]() {  // the rows behind the last token repeat the first one
       e = t.m.act[a];
@@ -124,7 +128,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           row[i] = token_at(t.m.mask[e], 4 * lane + i < n ? 4 * lane + i : 0);
     };
     if (work) enter();
-    for (long long b = b0; b < b1; ++b) {
+    for (int b = b0; b < b1; ++b) {
       if (!mbar_wait_warp(saddr(&t.empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
       const uint32_t fb = saddr(x_warp ? &t.full_x[stage] : &t.full[stage]);
       const uint32_t w = saddr(base + stage * g.stage_bytes);
@@ -170,9 +174,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     int stage = 0, it = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (long long b = b0; b < b1 && ok; ++it) {
-      const long long stop = min(b1, (b / g.kblocks + 1) * g.kblocks);
-      const int n_tok = few_count(t.m.mask[t.m.act[(int)(b / g.kblocks) / g.nt]]);
+    for (int b = b0; b < b1 && ok; ++it) {
+      const int stop = min(b1, (b / g.kblocks + 1) * g.kblocks);
+      const int n_tok = few_count(t.m.mask[t.m.act[b / g.kblocks / g.nt]]);
       const uint32_t idesc = idesc0 | ((uint32_t)((n_tok + 15) / 16 * 2) << 17);
       const int buf = it & 1;
       if (!mbar_wait_warp(saddr(&t.tempty[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag,
@@ -221,10 +225,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool first = et == 0;
     const int cl = q * 32 + lane;
     int it = 0, last_e = -1;
-    for (long long b = b0; b < b1; ++it) {
-      const int tile = (int)(b / g.kblocks);
-      const long long tile0 = (long long)tile * g.kblocks, tile1 = tile0 + g.kblocks;
-      const long long stop = min(b1, tile1);
+    for (int b = b0; b < b1; ++it) {
+      const int tile = b / g.kblocks;
+      const int tile0 = tile * g.kblocks, tile1 = tile0 + g.kblocks, stop = min(b1, tile1);
       const bool whole = b == tile0 && stop == tile1;
       const int a = tile / g.nt, e = t.m.act[a], ct = tile % g.nt;
       const int buf = it & 1;
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(saddr(&t.tempty[buf]));
       if (!whole) {
-        const int p0 = few_piece_of(tile0, total, pieces), p1 = few_piece_of(tile1 - 1, total, pieces);
+        const int p0 = cut.of(tile0), p1 = cut.of(tile1 - 1);
         __threadfence();
         epi_bar();
         if (first) t.last = atomicAdd(g.arrived + p0, 1u) == (unsigned)(p1 - p0);
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) gf[i] = uf[i] = 0.f;
             for (int p = p0; p <= p1; ++p) {
-              const int s = 2 * p + (tile0 >= few_piece_begin(p, total, pieces) ? 1 : 0);
+              const int s = 2 * p + (tile0 >= cut.begin(p) ? 1 : 0);
               const float* pp = g.part + ((size_t)s * g.T + j0) * 256 + cl;
 #pragma unroll
               for (int i = 0; i < 8; ++i)

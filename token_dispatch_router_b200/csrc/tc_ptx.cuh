@@ -104,6 +104,9 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
 }
 
 // ---------------------------------------------------------------- TMA and cp.async
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
                                             uint32_t bar) {
   asm volatile(
