@@ -28,7 +28,9 @@ moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void
                               AdapterTile* tiles, cudaStream_t st);
 moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
                                const void* in, const void* w, const AdapterTile* tiles,
-                               const void* low, const void* m, void* out, cudaStream_t st);
+                               const void* low, const void* m, void* out, float* part,
+                               cudaStream_t st);
+size_t adapter_gemm_part_bytes(int T, int k_dim, int n_out);
 size_t adapter_outer_part_bytes(int T, int d_in, int d_out, int r);
 moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
                                 const void* d_y, const void* planes_d_low,
@@ -59,7 +61,7 @@ moe_shape group_shape(const moe_adapter_shape& s) {
 
 struct Layout {
   size_t counts, offsets, a2p, rows, scratch;                    // grouping
-  size_t tiles, terms;                                           // for the large product
+  size_t tiles, terms, gemm_part;                                // for the large product
   size_t d_low, planes_d, planes_l, part, total_fwd, total;  // backward
 };
 Layout layout(const moe_adapter_shape& s) {
@@ -78,6 +80,9 @@ Layout layout(const moe_adapter_shape& s) {
   L.scratch = take(permute_scratch_bytes(group_shape(s)));
   L.tiles = take((T + kAdapterTileRows - 1) / kAdapterTileRows * sizeof(AdapterTile));
   L.terms = take(2 * T * r * 2);
+  const size_t pf = adapter_gemm_part_bytes(s.T, s.d_in, s.d_out);
+  const size_t pb = adapter_gemm_part_bytes(s.T, s.d_out, s.d_in);
+  L.gemm_part = take(pf > pb ? pf : pb);
   L.total_fwd = o;
   L.d_low = take(T * r * 4);
   L.planes_d = take(3 * T * r * 2);
@@ -133,7 +138,8 @@ moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, con
                               (AdapterTile*)(ws + L.tiles), st)) != MOE_OK)
     return r;
   return launch_adapter_gemm(false, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w,
-                             (const AdapterTile*)(ws + L.tiles), ws + L.terms, b, y, st);
+                             (const AdapterTile*)(ws + L.tiles), ws + L.terms, b, y,
+                             (float*)(ws + L.gemm_part), st);
 }
 
 moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, const void* x,
@@ -154,8 +160,8 @@ moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, 
     return r;
   if (d_x != nullptr &&
       (r = launch_adapter_gemm(true, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, d_y, w,
-                               (const AdapterTile*)(ws + L.tiles), ws + L.terms, a, d_x, st)) !=
-          MOE_OK)
+                               (const AdapterTile*)(ws + L.tiles), ws + L.terms, a, d_x,
+                               (float*)(ws + L.gemm_part), st)) != MOE_OK)
     return r;
   return launch_adapter_outer(s.T, s.d_in, s.d_out, s.rank, s.n_adapters, x, d_y,
                               ws + L.planes_d, ws + L.planes_l, offsets, rows, d_a, d_b,

@@ -38,7 +38,6 @@ struct Tail {
   uint64_t full[MAX_STAGES], full_x[MAX_STAGES], empty[MAX_STAGES], done;
   uint32_t tmem;
   int abort;
-  float low[8][128];  // projection: the low-rank values of the rows in hand
 };
 
 __device__ __forceinline__ float4 ld_dsmem_v4(uint32_t cluster_addr) {
@@ -61,7 +60,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   constexpr int LANES = BN / 4;     // lanes on a row of it, four columns each
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  Tail& t = *reinterpret_cast<Tail*>(base + g.ring_bytes);
+  Tail& t = *reinterpret_cast<Tail*>(base + g.ring_bytes + g.low_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &t.abort;
   const int S = g.split, rank = S > 1 ? (int)cluster_rank() : 0;
@@ -78,17 +77,24 @@ __global__ void __launch_bounds__(THREADS, 2)
     mbar_init_fence();
   }
   if (warp == 2) tmem_alloc<1>(saddr(&t.tmem), BN);
+  if (tid == 96) {
+    prefetch_map(&tmX);
+    prefetch_map(&tmW);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = t.tmem;
   const uint64_t limit = g.limit_ns;
+  const int mine = (g.T - rank + S - 1) / S;  // rows rank, rank + S, ... are this rank's
+  float* low = reinterpret_cast<float*>(base + g.ring_bytes);  // [mine][rank]
   const uint32_t x_piece = (uint32_t)(g.T + 7) / 8u * 1024u, x_bytes = PIECES * x_piece;
   const int b0 = rank * g.kb / S, b1 = (rank + 1) * g.kb / S;
 
   if (warp == 0 || warp == 1) {
     // ------------------------------------------------------------ loads
     const bool x_warp = warp == 1;
+    const uint64_t once = l2_policy_evict_first();  // W is read once
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_par = 0;
     for (int b = b0; b < b1; ++b) {
@@ -98,7 +104,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       if (elect_one()) {
         mbar_expect_tx(fb, x_warp ? x_bytes : (uint32_t)W_BYTES);
         if (x_warp) tma_load_4d(x, &tmX, 0, 0, b * PIECES, 0, fb);
-        else tma_load_4d(x + x_bytes, &tmW, 0, b * BK, tile * (BN / 64), 0, fb);
+        else tma_load_4d_hint(x + x_bytes, &tmW, 0, b * BK, tile * (BN / 64), 0, fb, once);
       }
       __syncwarp();
       issued_mask |= 1u << stage;
@@ -149,6 +155,20 @@ __global__ void __launch_bounds__(THREADS, 2)
   } else if (warp >= 4) {
     pdl_wait();  // the previous kernel in the stream has completed (low; order of writes to out)
     pdl_trigger();
+    // meanwhile: low of this rank's rows, and their adapters' pieces of B on their way to L2
+    for (int i = tid - 128; i < mine * g.rank; i += 128) {
+      const int tok = rank + S * (i / g.rank), j = i % g.rank, l = g.ids[tok];
+      float v = 0.f;
+      if (l >= 0 && l < g.n_adapters) {
+        for (int s = 0; s < g.low_splits; ++s)
+          v += g.low_part[((size_t)s * g.T + tok) * g.rank + j];
+        v *= g.scale[l];
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            g.b + ((size_t)l * g.rank + j) * g.d + n0));  // the first line of the piece
+      }
+      low[i] = v;
+      if (tile == 0) g.low[(size_t)tok * g.rank + j] = v;
+    }
   }
   __syncwarp();
   int w_ok = 0;
@@ -184,15 +204,16 @@ __global__ void __launch_bounds__(THREADS, 2)
     tmem_dealloc<1>(tmem, BN);
   }
   // ---- this rank's tokens: the partial rows of all ranks in rank order, four columns a lane
-  if (warp >= 4 && ok) {
+  if (ok) {
     // a warp takes 32 / LANES rows at a time
-    const int ew = warp - 4, sub = lane / LANES, c4 = lane % LANES * 4, col = n0 + c4;
+    const int sub = lane / LANES, c4 = lane % LANES * 4, col = n0 + c4;
     constexpr int PER = 32 / LANES;
-    for (int i0 = 0; rank + S * PER * (i0 + ew) < g.T; i0 += 4) {
-      const int tok = rank + S * (PER * (i0 + ew) + sub);
-      const bool row_on = tok < g.T;
+    for (int i0 = PER * warp; i0 < mine; i0 += PER * (THREADS / 32)) {
+      const int i = i0 + sub, tok = rank + S * i;
+      const bool row_on = i < mine;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       const uint32_t at = saddr(part) + (uint32_t)(((row_on ? tok : 0) * PITCH + c4) * 4);
+      const int l = row_on ? g.ids[tok] : -1;
       if (S > 1) {
         for (int r = 0; r < S; ++r) {
           const float4 v = ld_dsmem_v4(map_rank(at, (uint32_t)r));
@@ -201,33 +222,17 @@ __global__ void __launch_bounds__(THREADS, 2)
       } else {
         acc = *reinterpret_cast<const float4*>(part + (size_t)(row_on ? tok : 0) * PITCH + c4);
       }
-      {
-        const int l = row_on ? g.ids[tok] : -1;
-        const bool has = l >= 0 && l < g.n_adapters;
-        float* low = t.low[ew * PER + sub];
-        __syncwarp();  // the rows before are done with low
-        for (int j = lane % LANES; j < g.rank; j += LANES) {
-          float v = 0.f;
-          if (has) {
-            for (int s = 0; s < g.low_splits; ++s)
-              v += g.low_part[((size_t)s * g.T + tok) * g.rank + j];
-            v *= g.scale[l];
-          }
-          low[j] = v;
-          if (tile == 0 && row_on) g.low[(size_t)tok * g.rank + j] = v;
-        }
-        __syncwarp();
-        if (has && col < g.d) {
-          const bf16* bp = g.b + (size_t)l * g.rank * g.d + col;
+      if (l >= 0 && l < g.n_adapters && col < g.d) {
+        const bf16* bp = g.b + (size_t)l * g.rank * g.d + col;
+        const float* lw = low + (size_t)i * g.rank;
 #pragma unroll 8
-          for (int j = 0; j < g.rank; ++j) {
-            const uint2 raw = *reinterpret_cast<const uint2*>(bp + (size_t)j * g.d);
-            const float v = low[j];
-            acc.x = fmaf(v, __uint_as_float(raw.x << 16), acc.x);
-            acc.y = fmaf(v, __uint_as_float(raw.x & 0xffff0000u), acc.y);
-            acc.z = fmaf(v, __uint_as_float(raw.y << 16), acc.z);
-            acc.w = fmaf(v, __uint_as_float(raw.y & 0xffff0000u), acc.w);
-          }
+        for (int j = 0; j < g.rank; ++j) {
+          const uint2 raw = *reinterpret_cast<const uint2*>(bp + (size_t)j * g.d);
+          const float v = lw[j];
+          acc.x = fmaf(v, __uint_as_float(raw.x << 16), acc.x);
+          acc.y = fmaf(v, __uint_as_float(raw.x & 0xffff0000u), acc.y);
+          acc.z = fmaf(v, __uint_as_float(raw.y << 16), acc.z);
+          acc.w = fmaf(v, __uint_as_float(raw.y & 0xffff0000u), acc.w);
         }
       }
       if (row_on && col < g.d)
@@ -247,13 +252,15 @@ moe_status run_bn(AdapterFewArgs a, int d_in, const void* x, const void* w, cuda
   // at once: two CTAs an SM where two stages of each fit, else one.
   const int tiles = (a.d + BN - 1) / BN, sms = sm_count();
   a.stage_bytes = W_BYTES + PIECES * ((a.T + 7) / 8 * 1024);
-  const int fixed = 1024 + (int)sizeof(Tail);
+  int fixed = 1024 + (int)sizeof(Tail) + 8192;  // with a guess at low, for the choice
   const int most = SMEM_TWO - fixed >= 2 * a.stage_bytes ? 2 * sms - 16 : sms - 16;
   a.split = 1;
   while (a.split < 4 && 2 * a.split * tiles <= most && a.kb >= 4 * a.split) a.split *= 2;
+  a.low_bytes = ((a.T + a.split - 1) / a.split * a.rank * 4 + 15) / 16 * 16;
+  fixed = 1024 + (int)sizeof(Tail) + a.low_bytes;
   a.stages = ((a.split * tiles <= sms - 16 ? SMEM_ONE : SMEM_TWO) - fixed) / a.stage_bytes;
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
-  if (a.stages < 2) a.stages = 2;
+  if (a.stages < 2) a.stages = (SMEM_MAX - fixed) / a.stage_bytes >= 2 ? 2 : 1;
   a.ring_bytes = a.stages * a.stage_bytes;
   const int part = (a.T * (BN + 4) * 4 + 1023) / 1024 * 1024;  // the partial tile takes its place
   if (a.ring_bytes < part) a.ring_bytes = part;

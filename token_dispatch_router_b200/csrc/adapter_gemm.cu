@@ -36,6 +36,8 @@ constexpr int GROUP_M = 8;  // row tiles that share the W panels of a wave throu
 
 struct AdapterGemmArgs {
   int T, n_out, kblocks, mt, nt, rank;
+  int whole, split;          // tiles made whole; pairs that share the contraction of the others
+  float* part;               // [others][split][2 CTAs][64][128 rows][4]
   const AdapterTile* tiles;  // [mt]
   bf16* out;                 // [T, n_out]
   unsigned* status;
@@ -52,6 +54,18 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t adesc, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]),
       "r"(off[4]), "r"(off[5]), "r"(off[6]), "r"(off[7])
       : "memory");
+}
+
+// Work item w: a whole tile, or split `s` of one of the tiles behind the whole ones.
+struct Item {
+  int tile, s, k0, k1;
+  bool whole, adapters;  // the adapter term belongs to the last split
+};
+__device__ __forceinline__ Item item_of(int w, const AdapterGemmArgs& g) {
+  if (w < g.whole) return Item{w, 0, 0, g.kblocks, true, true};
+  const int v = w - g.whole, s = v % g.split;
+  return Item{g.whole + v / g.split, s, s * g.kblocks / g.split, (s + 1) * g.kblocks / g.split,
+              false, s == g.split - 1};
 }
 
 // Tile w: GROUP_M row tiles at a time, all column tiles of the group.
@@ -77,12 +91,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = (uint32_t*)(done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  volatile int* epi_flag = (volatile int*)(tmem_slot + 2);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int pair = (int)cluster_id_x(), npairs = (int)num_clusters_x();
-  const int total = g.mt * g.nt;
+  const int total = g.whole + (g.mt * g.nt - g.whole) * g.split;
   const uint64_t limit = g.limit_ns;
   // Ring stages after a tile's k-blocks: for each group of its adapters, low (nl stages, both
   // terms) and then nl stages an adapter; low's stages are freed with the group, so a group and
@@ -135,13 +150,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         return true;
       };
       for (int w = pair; w < total && ok; w += npairs) {
+        const Item it = item_of(w, g);
         int m, n;
-        tile_of(w, g.mt, g.nt, m, n);
+        tile_of(it.tile, g.mt, g.nt, m, n);
         const int m0 = m * PAIR_M + (int)rank * BM, n0 = n * BN + (int)rank * 128;
         const AdapterTile* at = g.tiles + m;
-        const int n_ad = at->n;
+        const int n_ad = it.adapters ? at->n : 0;
         uint32_t fb, a;
-        for (int kb = 0; kb < g.kblocks; ++kb) {
+        for (int kb = it.k0; kb < it.k1; ++kb) {
           if (!begin(STAGE_BYTES, fb, a)) break;
           const uint32_t b = a + A_BYTES;
           tma_load_2d_pair(a, &tmA, kb * BK, m0, fb);
@@ -209,17 +225,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_commit<2>(map_rank(saddr(&empty[s]), 1));
       };
       for (int w = pair; w < total && ok; w += npairs, ++it) {
+        const Item wi = item_of(w, g);
         int m, n;
-        tile_of(w, g.mt, g.nt, m, n);
+        tile_of(wi.tile, g.mt, g.nt, m, n);
         const AdapterTile* at = g.tiles + m;
-        const int n_ad = at->n;
+        const int n_ad = wi.adapters ? at->n : 0;
         const int buf = it & 1;
         const uint32_t use = (uint32_t)(it >> 1);
         if (!mbar_wait<true>(saddr(&tempty[buf]), (use & 1u) ^ 1u, abort_flag, g.status, limit))
           break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(buf * BN);
-        for (int kb = 0; kb < g.kblocks; ++kb) {
+        for (int kb = wi.k0; kb < wi.k1; ++kb) {
           const int s = next();
           if (s < 0) break;
           const uint32_t a = saddr(base + s * STAGE_BYTES), b = a + A_BYTES;
@@ -228,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_mma<2>(d, desc_sw128(a + kk * 32, 16, 1024),
                       BWD ? desc_sw128(b + kk * 32, 16, 1024)
                           : desc_sw128(b + kk * 2048, B_CHUNK, 1024),
-                      idesc, (kb | kk) != 0 ? 1u : 0u);
+                      idesc, (kb > wi.k0 || kk > 0) ? 1u : 0u);
           release(s);
         }
         int low[2] = {0, 0};
@@ -271,23 +288,32 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
+    // One thread waits for all four warps, so that they leave a wait that ran out together.
     const int q = warp & 3;  // TMEM lanes 32 q ...
+    const bool first = tid == 64;
     const uint32_t tempty_leader = map_rank(saddr(&tempty[0]), 0);
     int it = 0;
     for (int w = pair; w < total; w += npairs, ++it) {
+      const Item wi = item_of(w, g);
       int m, n;
-      tile_of(w, g.mt, g.nt, m, n);
+      tile_of(wi.tile, g.mt, g.nt, m, n);
       const int buf = it & 1;
       const uint32_t use = (uint32_t)(it >> 1);
-      int w_ok = 0;
-      if (lane == 0)
-        w_ok = mbar_wait<true>(saddr(&tfull[buf]), use & 1u, abort_flag, g.status, limit);
-      w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
-      if (!w_ok) break;
+      if (first)
+        *epi_flag = mbar_wait<true>(saddr(&tfull[buf]), use & 1u, abort_flag, g.status, limit);
+      epi_bar();
+      const int ok = *epi_flag;
+      epi_bar();  // everyone has read it
+      if (!ok) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + (uint32_t)(buf * BN) + ((uint32_t)(q * 32) << 16);
-      const int r = m * PAIR_M + (int)rank * BM + q * 32 + lane;
+      const int lr = q * 32 + lane, r = m * PAIR_M + (int)rank * BM + lr;
       bf16* orow = g.out + (size_t)min(r, g.T - 1) * g.n_out;
+      // a split's partial: [4 columns][row][4]
+      float4* part = reinterpret_cast<float4*>(g.part) +
+                     (wi.whole ? 0
+                               : ((size_t)((wi.tile - g.whole) * g.split + wi.s) * 2 + rank) *
+                                     (BN / 4) * BM) + lr;
 #pragma unroll 1
       for (int c = 0; c < BN / 32; ++c) {
         const int col = n * BN + c * 32;
@@ -295,7 +321,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t v[32];
         tmem_ld32(tb + c * 32, v);
         tmem_ld_wait();
-        if (r < g.T) {
+        if (!wi.whole) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            part[(size_t)(c * 8 + j) * BM] =
+                make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                            __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+        } else if (r < g.T) {
           uint4* dst = reinterpret_cast<uint4*>(orow + col);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -321,6 +353,32 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// The tiles behind the whole ones: their splits' partials in order, eight columns of a row a
+// thread. CTA (row and column group, tile).
+constexpr int SUM_THREADS = 256;
+__global__ void __launch_bounds__(SUM_THREADS) adapter_gemm_sum_kernel(const AdapterGemmArgs g) {
+  const int i = (int)blockIdx.x * SUM_THREADS + (int)threadIdx.x, tile = g.whole + (int)blockIdx.y;
+  const int lr = i % BM, c8 = i / BM % (BN / 8), half = i / BM / (BN / 8);
+  int m, n;
+  tile_of(tile, g.mt, g.nt, m, n);
+  const int r = m * PAIR_M + half * BM + lr, col = n * BN + c8 * 8;
+  pdl_wait();  // the previous kernel in the stream has completed
+  pdl_trigger();
+  if (r >= g.T || col >= g.n_out) return;
+  const float4* p0 = reinterpret_cast<const float4*>(g.part) +
+                     ((size_t)blockIdx.y * g.split * 2 + half) * (BN / 4) * BM +
+                     (size_t)c8 * 2 * BM + lr;
+  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int s = 0; s < g.split; ++s) {
+    const float4* pp = p0 + (size_t)s * 2 * (BN / 4) * BM;
+    const float4 u = __ldcg(pp), v = __ldcg(pp + BM);
+    f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
+    f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
+  }
+  *reinterpret_cast<uint4*>(g.out + (size_t)r * g.n_out + col) = pack16(f, bf16());
+}
+
 template <bool BWD>
 moe_status run(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& ml,
                const CUtensorMap& mm, const AdapterGemmArgs& a, cudaStream_t st) {
@@ -328,21 +386,54 @@ moe_status run(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& 
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
-  int pairs = sm_count() / 2;
-  if (pairs > a.mt * a.nt) pairs = a.mt * a.nt;
+  const int items = a.whole + (a.mt * a.nt - a.whole) * a.split;
+  const int pairs = items < sm_count() / 2 ? items : sm_count() / 2;
   launch_begin(K_ADAPTER_GEMM, st);
   launch_kernel(kern, dim3((unsigned)(2 * pairs)), dim3(THREADS), (size_t)SMEM_BYTES, st, 2, ma,
                 mb, ml, mm, a);
-  return launch_end(K_ADAPTER_GEMM, st);
+  const moe_status s = launch_end(K_ADAPTER_GEMM, st);
+  if (s != MOE_OK || a.split == 1) return s;
+  launch_begin(K_ADAPTER_GEMM_SUM, st);
+  launch_kernel(adapter_gemm_sum_kernel,
+                dim3(PAIR_M * BN / 8 / SUM_THREADS, (unsigned)(a.mt * a.nt - a.whole)),
+                dim3(SUM_THREADS), 0, st, 1, a);
+  return launch_end(K_ADAPTER_GEMM_SUM, st);
 }
 
 }  // namespace
+
+// Tiles that do not fill the pairs of SMs once more are cut along the contraction, so that they
+// take that part of a tile's time: at most eight splits of at least four k-blocks, whose fp32
+// partials a second kernel adds in order. (2880 x 2880, 2049 rows: 108 tiles on 74 pairs took two
+// rounds.) Returns the number of partials.
+int adapter_gemm_split(int T, int k_dim, int n_out, int* whole, int* split) {
+  const int pairs = sm_count() / 2;
+  const int tiles = ((T + PAIR_M - 1) / PAIR_M) * ((n_out + BN - 1) / BN);
+  const int rest = tiles % pairs;
+  int s = rest > 0 ? pairs / rest : 1;
+  if (s > k_dim / BK / 4) s = k_dim / BK / 4;
+  if (s > 8) s = 8;
+  // the second kernel takes about 4 us, a k-block 0.29 (300 rows, 768 -> 2048: 27 us whole, 30 cut)
+  if (s < 2 || (k_dim / BK) * (s - 1) < 20 * s) {
+    *whole = tiles;
+    *split = 1;
+    return 0;
+  }
+  *whole = tiles - rest;
+  *split = s;
+  return rest * s;
+}
+size_t adapter_gemm_part_bytes(int T, int k_dim, int n_out) {
+  int whole, split;
+  return (size_t)adapter_gemm_split(T, k_dim, n_out, &whole, &split) * PAIR_M * BN * 4;
+}
 
 // in [T, k_dim], w [d_in, d_out]; forward: k_dim = d_in, out [T, d_out], m = B; backward:
 // k_dim = d_out, out [T, d_in], m = A. low: [2][T][rank] bf16 terms.
 moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
                                const void* in, const void* w, const AdapterTile* tiles,
-                               const void* low, const void* m, void* out, cudaStream_t st) {
+                               const void* low, const void* m, void* out, float* part,
+                               cudaStream_t st) {
   AdapterGemmArgs a = {};
   const int k_dim = bwd ? d_out : d_in, n_out = bwd ? d_in : d_out;
   a.T = T;
@@ -351,6 +442,8 @@ moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapt
   a.mt = (T + PAIR_M - 1) / PAIR_M;
   a.nt = (n_out + BN - 1) / BN;
   a.rank = rank;
+  adapter_gemm_split(T, k_dim, n_out, &a.whole, &a.split);
+  a.part = part;
   a.tiles = tiles;
   a.out = (bf16*)out;
   a.status = device_status_ptr();

@@ -81,6 +81,4 @@ struct FewPieces {
   }
 };
 
-// Four epilogue warps (barrier 1).
-__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 }  // namespace moe

@@ -41,7 +41,7 @@ struct AdapterFewArgs {
   int rank, low_splits, n_adapters;
   bf16* out;               // [T, d]
   // set by the launcher
-  int kb, split, stages, stage_bytes, ring_bytes;
+  int kb, split, stages, stage_bytes, ring_bytes, low_bytes;
   unsigned* status;
   unsigned long long limit_ns;
 };
