@@ -10,8 +10,9 @@
 // to 2^-24, so the fp32 gradients lose nothing; the tensor pipe has the time (three MMAs of
 // N = r for each 32 x 256 tile of wide rows).
 //
-// A unit is (adapter, chunk of its rows, 256 columns of x or of d_y); several are resident on an
-// SM so that one loads while another stores. Chunks of one adapter leave partial sums that a
+// A unit is (adapter, chunk of its rows, 256 columns of x or of d_y). Two CTAs an SM run through
+// the units, each with two pairs of accumulators, so that loads run on while a unit is stored
+// (many adapters have only a few rows each). Chunks of one adapter leave partial sums that a
 // second kernel adds in chunk order (results repeat bit for bit); it is launched only where an
 // adapter can have two chunks. An adapter without rows has one empty chunk, which writes zeros.
 // Every wait is bounded (MOE_ERR_TIMEOUT on expiry).
@@ -24,12 +25,13 @@ namespace {
 
 using namespace ptx;
 
-constexpr int LOADERS = 128, THREADS = 192;  // four gather / store warps, MMA warp, TMA warp
+constexpr int LOADERS = 128, THREADS = 320;  // four gather warps, MMA, TMA, four store warps
 constexpr int OC = 256;                      // columns of a unit
 constexpr int OT = 32;                       // rows per stage
 constexpr int STAGES = 3;
 constexpr int CHUNK = OT * 128;              // OT rows x 64 columns
 constexpr int BIG_BYTES = OC / 64 * CHUNK;   // 16 KB
+constexpr int kMaxAdapters = 256;
 
 struct OuterArgs {
   const bf16* big[2];     // x [T, D0], d_y [T, D1]
@@ -46,145 +48,178 @@ struct OuterArgs {
   unsigned long long limit_ns;
 };
 
+struct Table {
+  int chunk0[kMaxAdapters + 1];  // first chunk of each adapter
+  int multi0[kMaxAdapters];      // its first place among the chunks that leave partials
+};
+struct Unit {
+  int l, p, c0, lo, n, slot;  // adapter, side, first column, first slot, rows; partial (-1: whole)
+};
+
+__device__ __forceinline__ void make_table(Table& t, const OuterArgs& g) {  // one warp
+  const int lane = threadIdx.x & 31;
+  int run = 0, mrun = 0;
+  for (int l0 = 0; l0 < g.L; l0 += 32) {
+    const int l = l0 + lane;
+    const int c = l < g.L ? g.offsets[l + 1] - g.offsets[l] : 0;
+    const int n = l < g.L ? max(1, (c + g.chunk - 1) / g.chunk) : 0, m = n > 1 ? n : 0;
+    int incl = n, mincl = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int w = __shfl_up_sync(0xffffffffu, mincl, o);
+      if (lane >= o) {
+        incl += v;
+        mincl += w;
+      }
+    }
+    if (l < g.L) {
+      t.chunk0[l] = run + incl - n;
+      t.multi0[l] = mrun + mincl - m;
+    }
+    run += __shfl_sync(0xffffffffu, incl, 31);
+    mrun += __shfl_sync(0xffffffffu, mincl, 31);
+  }
+  if (lane == 0) t.chunk0[g.L] = run;
+}
+__device__ __forceinline__ Unit unit_of(int u, const Table& t, const OuterArgs& g) {
+  const int nct = g.tiles[0] + g.tiles[1], cg = u / nct, ct = u % nct;
+  int lo = 0, hi = g.L - 1;  // the last adapter whose chunks begin at cg or before
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.chunk0[mid] <= cg) lo = mid;
+    else hi = mid - 1;
+  }
+  Unit v;
+  v.l = lo;
+  const int i = cg - t.chunk0[lo], first = g.offsets[lo] + i * g.chunk;
+  v.p = ct >= g.tiles[0] ? 1 : 0;
+  v.c0 = (ct - (v.p ? g.tiles[0] : 0)) * OC;
+  v.lo = first;
+  v.n = max(0, min(g.chunk, g.offsets[lo + 1] - first));
+  v.slot = t.chunk0[lo + 1] - t.chunk0[lo] > 1 ? t.multi0[lo] + i : -1;
+  return v;
+}
+
 __global__ void __launch_bounds__(THREADS)
     adapter_outer_kernel(const __grid_constant__ CUtensorMap tmP0,
                          const __grid_constant__ CUtensorMap tmP1, const OuterArgs g) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[STAGES], empty[STAGES], done;
+  __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_l, s_i, s_n, s_base, s_abort;
+  __shared__ int s_abort;
+  __shared__ Table table;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sb = (saddr(smem_raw) + 1023u) & ~1023u;
   const int p_bytes = g.nc * CHUNK, st_bytes = BIG_BYTES + 3 * p_bytes;
   volatile int* abort_flag = &s_abort;
-  // Two accumulators of 128 columns; for ranks up to 64 two pairs, taken in turn by the k steps
-  // (MMAs into one accumulator follow each other about 190 cycles apart however small they are)
-  const int pairs = g.nc == 1 ? 2 : 1;
-  const uint32_t tcols = tmem_columns(2 * pairs * g.n_mma);
+  const uint32_t tcols = tmem_columns(4 * g.n_mma);
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(saddr(&full[s]), LOADERS + 1);
       mbar_init(saddr(&empty[s]), 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(saddr(&tfull[b]), 1);
+      mbar_init(saddr(&tempty[b]), 4);  // the store warps
+    }
     mbar_init(saddr(&done), 1);
     s_abort = 0;
-    s_l = -1;
     mbar_init_fence();
   }
-  __syncthreads();
+  if (warp == 4) tmem_alloc<1>(saddr(&s_tmem), tcols);
+  if (tid == 32) {
+    prefetch_map(&tmP0);
+    prefetch_map(&tmP1);
+  }
   pdl_wait();  // the previous kernel in the stream has completed
   pdl_trigger();
-  const int nct = g.tiles[0] + g.tiles[1];
-  const int cg = blockIdx.x / nct, ct = blockIdx.x % nct;  // chunk, column tile
-  if (warp == 0) {  // chunk cg: adapter, index in it, its chunks, first partial slot
-    int run = 0, mrun = 0;
-    for (int l0 = 0; l0 < g.L; l0 += 32) {
-      const int l = l0 + lane;
-      const int c = l < g.L ? g.offsets[l + 1] - g.offsets[l] : 0;
-      const int n = l < g.L ? max(1, (c + g.chunk - 1) / g.chunk) : 0;
-      const int m = n > 1 ? n : 0;
-      int incl = n, mincl = m;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        const int w = __shfl_up_sync(0xffffffffu, mincl, o);
-        if (lane >= o) {
-          incl += v;
-          mincl += w;
-        }
-      }
-      const int mine = run + incl - n;
-      if (cg >= mine && cg < mine + n) {
-        s_l = l;
-        s_i = cg - mine;
-        s_n = n;
-        s_base = mrun + mincl - m;
-      }
-      run += __shfl_sync(0xffffffffu, incl, 31);
-      mrun += __shfl_sync(0xffffffffu, mincl, 31);
-    }
-  }
-  __syncthreads();
-  const int l = s_l;
-  if (l < 0) return;  // past the last chunk
-  if (warp == 4) tmem_alloc<1>(saddr(&s_tmem), tcols);
+  if (warp == 0) make_table(table, g);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int p = ct >= g.tiles[0] ? 1 : 0;
-  const int c0 = (ct - (p ? g.tiles[0] : 0)) * OC, D = g.D[p];
-  const int lo = g.offsets[l] + s_i * g.chunk;
-  const int n = max(0, min(g.chunk, g.offsets[l + 1] - lo));
-  const int steps = (n + OT - 1) / OT;
   const uint64_t limit = g.limit_ns;
-  bool ok = true;
+  const int units = table.chunk0[g.L] * (g.tiles[0] + g.tiles[1]), step = (int)gridDim.x;
 
   if (warp < 4) {
     // ------------------------------------------------------------ gather
     // wide rows: warp w copies rows w, w + 4, ..., 512 bytes (one 16-byte piece a lane) each
-    const bf16* big = g.big[p] + c0 + lane * 8;
-    const bool col_on = c0 + lane * 8 < D;
-    const int chunk_at = (lane >> 3) * CHUNK;
-    const bf16* planes = g.planes[p];
+    const int chunk_at = (lane >> 3) * CHUNK, pieces = g.n_mma / 8;
     const size_t plane = (size_t)g.T * g.r;
-    const int pieces = g.n_mma / 8;
-    // lane i < 8 holds the row of this warp's i-th row in the next stage
-    auto row_of = [&](int s) {
-      const int r = s * OT + warp + 4 * (lane & 7);
-      return r < n ? g.rows[lo + r] : -1;
-    };
-    int ahead = steps > 0 ? row_of(0) : -1;
     int stage = 0;
     uint32_t phase = 0;
-    for (int s = 0; s < steps; ++s) {
-      const int mine = ahead;
-      if (s + 1 < steps) ahead = row_of(s + 1);
-      if (!mbar_wait_warp(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) {
-        ok = false;
-        break;
-      }
-      const uint32_t bs = sb + stage * st_bytes, ps = bs + BIG_BYTES;
-#pragma unroll
-      for (int i = 0; i < OT / 4; ++i) {
-        const int t = __shfl_sync(0xffffffffu, mine, i), r = warp + 4 * i;
-        const bool on = t >= 0 && col_on;
-        cp_async16_if(bs + chunk_at + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                      on ? big + (size_t)t * D : g.big[p], on);
-      }
-      if ((s + 1) * OT > n)  // the last rows: the slots behind them are another adapter's
-        for (int i = tid; i < 3 * OT * pieces; i += LOADERS) {
-          const int q = i / (OT * pieces), r = i / pieces % OT, c = i % pieces;
-          const bool on = s * OT + r < n && c * 8 < g.r;
-          cp_async16_if(ps + q * p_bytes + (c >> 3) * CHUNK + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                        planes + (on ? q * plane + (size_t)(lo + s * OT + r) * g.r + c * 8 : 0),
-                        on);
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += step) {
+      const Unit v = unit_of(u, table, g);
+      const int steps = (v.n + OT - 1) / OT, D = g.D[v.p];
+      const bf16* big = g.big[v.p] + v.c0 + lane * 8;
+      const bool col_on = v.c0 + lane * 8 < D;
+      // lane i < 8 holds the row of this warp's i-th row in the next stage
+      auto row_of = [&](int s) {
+        const int r = s * OT + warp + 4 * (lane & 7);
+        return r < v.n ? g.rows[v.lo + r] : -1;
+      };
+      int ahead = steps > 0 ? row_of(0) : -1;
+      for (int s = 0; s < steps; ++s) {
+        const int mine = ahead;
+        if (s + 1 < steps) ahead = row_of(s + 1);
+        if (!mbar_wait_warp(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) {
+          ok = false;
+          break;
         }
-      cp_async_arrive_noinc(saddr(&full[stage]));
-      if (++stage == STAGES) {
-        stage = 0;
-        phase ^= 1u;
+        const uint32_t bs = sb + stage * st_bytes, ps = bs + BIG_BYTES;
+#pragma unroll
+        for (int i = 0; i < OT / 4; ++i) {
+          const int t = __shfl_sync(0xffffffffu, mine, i), r = warp + 4 * i;
+          const bool on = t >= 0 && col_on;
+          cp_async16_if(bs + chunk_at + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                        on ? big + (size_t)t * D : g.big[v.p], on);
+        }
+        if ((s + 1) * OT > v.n)  // the last rows: the slots behind them are another adapter's
+          for (int i = tid; i < 3 * OT * pieces; i += LOADERS) {
+            const int q = i / (OT * pieces), r = i / pieces % OT, c = i % pieces;
+            const bool on = s * OT + r < v.n && c * 8 < g.r;
+            cp_async16_if(
+                ps + q * p_bytes + (c >> 3) * CHUNK + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                g.planes[v.p] + (on ? q * plane + (size_t)(v.lo + s * OT + r) * g.r + c * 8 : 0),
+                on);
+          }
+        cp_async_arrive_noinc(saddr(&full[stage]));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
     cp_async_wait_all();
   } else if (warp == 5) {
     // ------------------------------------------------------------ low-rank terms (TMA)
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+    int stage = 0;
+    uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += step) {
+      const Unit v = unit_of(u, table, g);
+      const int steps = (v.n + OT - 1) / OT;
       for (int s = 0; s < steps; ++s) {
-        if (!mbar_wait(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
-        const uint32_t fb = saddr(&full[stage]), ps = sb + stage * st_bytes + BIG_BYTES;
-        if ((s + 1) * OT <= n) {
-          mbar_expect_tx(fb, (uint32_t)(3 * p_bytes));
-          for (int q = 0; q < 3; ++q)
-            for (int c = 0; c < g.nc; ++c)
-              tma_load_3d(ps + q * p_bytes + c * CHUNK, p ? &tmP1 : &tmP0, 64 * c, lo + s * OT, q,
-                          fb);
-        } else {
-          mbar_arrive(fb);  // the gather warps copy these
+        if (!mbar_wait_warp(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) {
+          ok = false;
+          break;
         }
+        if (elect_one()) {
+          const uint32_t fb = saddr(&full[stage]), ps = sb + stage * st_bytes + BIG_BYTES;
+          if ((s + 1) * OT <= v.n) {
+            mbar_expect_tx(fb, (uint32_t)(3 * p_bytes));
+            for (int q = 0; q < 3; ++q)
+              for (int c = 0; c < g.nc; ++c)
+                tma_load_3d(ps + q * p_bytes + c * CHUNK, v.p ? &tmP1 : &tmP0, 64 * c,
+                            v.lo + s * OT, q, fb);
+          } else {
+            mbar_arrive(fb);  // the gather warps copy these
+          }
+        }
+        __syncwarp();
         issued_mask |= 1u << stage;
         issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
         if (++stage == STAGES) {
@@ -192,6 +227,8 @@ __global__ void __launch_bounds__(THREADS)
           phase ^= 1u;
         }
       }
+    }
+    if (lane == 0)
       for (int s = 0; s < STAGES; ++s) {  // nothing of ours is in flight after this (bounded)
         if (!(issued_mask & (1u << s))) continue;
         const uint64_t t0 = globaltimer_ns();
@@ -199,85 +236,102 @@ __global__ void __launch_bounds__(THREADS)
                globaltimer_ns() - t0 < limit) {
         }
       }
-    }
-  } else {
+  } else if (warp == 4) {
     // ------------------------------------------------------------ MMA issuer
     // D fp32, A and B bf16, both MN-major (bits 15 and 16), M = 128, N = n_mma
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                            ((uint32_t)(g.n_mma >> 3) << 17) | (8u << 24);
     const uint64_t bd0 = desc_sw128(sb, CHUNK, 1024), pd0 = desc_sw128(sb + BIG_BYTES, CHUNK, 1024);
-    int stage = 0;
+    int stage = 0, it = 0;
     uint32_t phase = 0;
-    for (int s = 0; s < steps; ++s) {
-      if (!mbar_wait_warp(saddr(&full[stage]), phase, abort_flag, g.status, limit)) break;
-      fence_proxy_async_smem();  // the gathered rows (cp.async) -> MMA reads
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += step, ++it) {
+      const Unit v = unit_of(u, table, g);
+      const int steps = (v.n + OT - 1) / OT, buf = it & 1;
+      if (!mbar_wait_warp(saddr(&tempty[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag,
+                          g.status, limit))
+        break;
       tc_fence_after();
-      if (elect_one()) {
-        const uint64_t so = (uint64_t)((stage * st_bytes) >> 4);
+      const uint32_t acc = tmem + (uint32_t)(buf * 2 * g.n_mma);
+      for (int s = 0; s < steps; ++s) {
+        if (!mbar_wait_warp(saddr(&full[stage]), phase, abort_flag, g.status, limit)) {
+          ok = false;
+          break;
+        }
+        fence_proxy_async_smem();  // the gathered rows (cp.async) -> MMA reads
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t so = (uint64_t)((stage * st_bytes) >> 4);
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+          for (int q = 0; q < 3; ++q)
 #pragma unroll
-          for (int kk = 0; kk < OT / 16; ++kk)
+            for (int kk = 0; kk < OT / 16; ++kk)
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const int acc = 2 * (kk & (pairs - 1)) + m;
-              tc_mma<1>(tmem + (uint32_t)(acc * g.n_mma),
-                        bd0 + so + (uint64_t)((m * 2 * CHUNK + kk * 2048) >> 4),
-                        pd0 + so + (uint64_t)((q * p_bytes + kk * 2048) >> 4), idesc,
-                        (s > 0 || q > 0 || kk >= pairs) ? 1u : 0u);
-            }
-        tc_commit<1>(saddr(&empty[stage]));
-      }
-      __syncwarp();
-      if (++stage == STAGES) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-    if (elect_one()) tc_commit<1>(saddr(&done));
-  }
-  __syncwarp();
-  int w_ok = 0;
-  if (lane == 0) w_ok = mbar_wait(saddr(&done), 0, nullptr, g.status, limit);
-  ok = __shfl_sync(0xffffffffu, w_ok, 0) && ok && !*abort_flag;
-  tc_fence_after();
-
-  if (warp < 4) {
-    // ------------------------------------------------------------ store
-    const size_t wide = (size_t)(g.D[0] + g.D[1]) * g.r, at = p ? (size_t)g.D[0] * g.r : 0;
-    const bool direct = s_n == 1;
-    float* out = g.out[p] + (size_t)l * D * g.r;
-    float* dst = direct ? out : g.part + (size_t)(s_base + s_i) * wide + at;
-#pragma unroll 1
-    for (int m = 0; m < 2; ++m) {
-      const int c = c0 + m * 128 + warp * 32 + lane;
-#pragma unroll 1
-      for (int j0 = 0; j0 < g.r; j0 += 8) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = 0.f;
-        if (steps > 0)
-          for (int h = 0; h < pairs; ++h) {
-            uint32_t v[8];
-            tmem_ld8(tmem + (uint32_t)((2 * h + m) * g.n_mma + j0) +
-                         ((uint32_t)(warp * 32) << 16), v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] += __uint_as_float(v[j]);
-          }
-        if (c >= D || !ok) continue;
-        if (p == 0) {
-          float4* o = reinterpret_cast<float4*>(dst + (size_t)c * g.r + j0);
-          o[0] = make_float4(f[0], f[1], f[2], f[3]);
-          o[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dst[(size_t)(j0 + j) * D + c] = f[j];
+              for (int m = 0; m < 2; ++m)
+                tc_mma<1>(acc + (uint32_t)(m * g.n_mma),
+                          bd0 + so + (uint64_t)((m * 2 * CHUNK + kk * 2048) >> 4),
+                          pd0 + so + (uint64_t)((q * p_bytes + kk * 2048) >> 4), idesc,
+                          (s > 0 || q > 0 || kk > 0) ? 1u : 0u);
+          tc_commit<1>(saddr(&empty[stage]));
+        }
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
+      if (ok && elect_one()) tc_commit<1>(saddr(&tfull[buf]));
+      __syncwarp();
+    }
+    if (elect_one()) tc_commit<1>(saddr(&done));
+    __syncwarp();
+    if (lane == 0) {  // every MMA has completed before TMEM is freed (bounded)
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try(saddr(&done), 0) && globaltimer_ns() - t0 < limit) {
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ store
+    const int q = warp & 3;  // TMEM lanes 32 q ...: columns of x or d_y
+    const size_t wide = (size_t)(g.D[0] + g.D[1]) * g.r;
+    int it = 0;
+    for (int u = blockIdx.x; u < units; u += step, ++it) {
+      const Unit v = unit_of(u, table, g);
+      const int buf = it & 1, D = g.D[v.p];
+      float* dst = v.slot < 0 ? g.out[v.p] + (size_t)v.l * D * g.r
+                              : g.part + (size_t)v.slot * wide + (v.p ? (size_t)g.D[0] * g.r : 0);
+      if (!mbar_wait_warp(saddr(&tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, g.status,
+                          limit))
+        break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t)(buf * 2 * g.n_mma) + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+      for (int m = 0; m < 2; ++m) {
+        const int c = v.c0 + m * 128 + q * 32 + lane;
+#pragma unroll 2
+        for (int j0 = 0; j0 < g.r; j0 += 8) {
+          uint32_t f[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+          if (v.n > 0) {  // else no rows: zeros
+            tmem_ld8(acc + (uint32_t)(m * g.n_mma + j0), f);
+            tmem_ld_wait();
+          }
+          if (c >= D) continue;
+          if (v.p == 0) {
+            uint4* o = reinterpret_cast<uint4*>(dst + (size_t)c * g.r + j0);
+            o[0] = make_uint4(f[0], f[1], f[2], f[3]);
+            o[1] = make_uint4(f[4], f[5], f[6], f[7]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dst[(size_t)(j0 + j) * D + c] = __uint_as_float(f[j]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(saddr(&tempty[buf]));
     }
   }
-  __syncwarp();
+  __syncwarp();  // lanes that waited alone are back
   tc_fence_before();
   __syncthreads();
   if (warp == 4) {
@@ -386,8 +440,11 @@ moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const 
   if (!make_map(&m0, planes_d_low, 3, pd, ps, pbox) || !make_map(&m1, planes_low, 3, pd, ps, pbox))
     return MOE_ERR_CUDA;
   launch_begin(K_ADAPTER_OUTER, st);
-  launch_kernel(adapter_outer_kernel, dim3((unsigned)((T / a.chunk + L) * (a.tiles[0] + a.tiles[1]))),
-                dim3(THREADS), (size_t)smem, st, 1, m0, m1, a);
+  // two CTAs an SM (one for a rank above 64, whose accumulators take all of TMEM)
+  const long long most = (long long)(T / a.chunk + L) * (a.tiles[0] + a.tiles[1]);
+  const int ctas = (a.nc == 1 ? 2 : 1) * sm_count();
+  launch_kernel(adapter_outer_kernel, dim3((unsigned)(most < ctas ? most : ctas)), dim3(THREADS),
+                (size_t)smem, st, 1, m0, m1, a);
   const moe_status s = launch_end(K_ADAPTER_OUTER, st);
   if (s != MOE_OK || T <= a.chunk) return s;
   const size_t wide = (size_t)(d_in + d_out) * r;
