@@ -118,3 +118,269 @@ def test_backward_matches_the_definition(cuda_lib, T, d_in, d_out, L, r, ids):
         eb = n * F32 * (low[t].double().abs().t() @ d_y[t].abs())
         assert ((d_a[l].double() - ra).abs() <= ea).all(), ("d_a", l)
         assert ((d_b[l].double() - rb).abs() <= eb).all(), ("d_b", l)
+
+
+def backward(tdr, s, inp, low, **kw):
+    return tdr.adapter_backward(s, inp["d_y"], inp["x"], inp["w"], inp["a"], inp["b"], inp["ids"],
+                                inp["scale"], low, **kw)
+
+
+@pytest.mark.parametrize("T", [5, 128, 300, 1000])
+def test_a_broken_adapter_or_row_stays_alone(cuda_lib, T):
+    """NaN and infinity in one adapter, or one row, reach its own rows and gradients only."""
+    tdr = cuda_lib
+    d_in, d_out, L, r = 512, 704, 7, 24
+    inp = make(T, d_in, d_out, L, r, T)
+    s, (y, low, _) = call_forward(tdr, inp)
+    d_x, d_a, d_b = backward(tdr, s, inp, low)
+    ids = inp["ids"]
+    for l, name, value in ((0, "a", torch.nan), (L - 1, "b", torch.inf), (3, "b", torch.nan)):
+        sick = dict(inp, **{name: inp[name].clone()})
+        sick[name][l] = value
+        _, (y2, low2, _) = call_forward(tdr, sick)
+        own = ids == l
+        assert torch.equal(y2[~own], y[~own]) and not y2[own].isfinite().any()
+        x2, a2, b2 = backward(tdr, s, sick, low)
+        assert torch.equal(x2[~own], d_x[~own]) and not x2[own].isfinite().any()
+        keep = torch.arange(L, device="cuda") != l
+        assert torch.equal(a2[keep], d_a[keep]) and torch.equal(b2, d_b)
+    t = int((ids >= 0).nonzero()[0, 0])
+    sick = dict(inp, x=inp["x"].clone(), d_y=inp["d_y"].clone())
+    sick["x"][t], sick["d_y"][t] = torch.nan, torch.inf
+    _, (y2, low2, _) = call_forward(tdr, sick)
+    rest = torch.arange(T, device="cuda") != t
+    assert torch.equal(y2[rest], y[rest]) and torch.equal(low2[rest], low[rest])
+    assert y2[t].isnan().all()
+    x2, a2, b2 = backward(tdr, s, sick, low)
+    assert torch.equal(x2[rest], d_x[rest]) and not x2[t].isfinite().any()
+    keep = torch.arange(L, device="cuda") != ids[t]
+    assert torch.equal(a2[keep], d_a[keep]) and torch.equal(b2[keep], d_b[keep])
+
+
+@pytest.mark.parametrize("T", [1, 77, 129, 2500])
+def test_workspace_outputs_and_repetition(cuda_lib, T):
+    tdr = cuda_lib
+    inp = make(T, 576, 320, 9, 16, T, "runs")
+    s, (y, low, _) = call_forward(tdr, inp)
+    grads = backward(tdr, s, inp, low)
+    ws = torch.full((tdr.adapter_workspace_size(s),), 255, dtype=torch.uint8, device="cuda")  # NaN
+    whole = torch.full((T + 2, 320), 3.0, dtype=torch.bfloat16, device="cuda")
+    for _ in range(4):
+        y2, low2, _ = call_forward(tdr, inp, workspace=ws, out=whole[1:T + 1])[1]
+        assert torch.equal(y2, y) and torch.equal(low2, low)
+        for p, q in zip(backward(tdr, s, inp, low, workspace=ws), grads):
+            assert torch.equal(p, q)
+        ws.fill_(255)
+    assert (whole[0] == 3).all() and (whole[T + 1] == 3).all()
+    d_x, d_a, d_b = backward(tdr, s, inp, low, want_d_x=False)
+    assert d_x is None and torch.equal(d_a, grads[1]) and torch.equal(d_b, grads[2])
+    assert tdr.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [100, 400])
+def test_ids_out_of_range_count_as_none_and_are_reported(cuda_lib, T):
+    tdr = cuda_lib
+    inp = make(T, 128, 128, 4, 8, 1)
+    none = dict(inp, ids=inp["ids"].clone())
+    none["ids"][[3, 50]] = -1
+    _, (y, low, _) = call_forward(tdr, none)
+    assert tdr.device_status() == 0
+    sick = dict(inp, ids=none["ids"].clone())
+    sick["ids"][3], sick["ids"][50] = 4, -2
+    _, (y2, low2, _) = call_forward(tdr, sick)
+    assert tdr.device_status() == 6
+    assert torch.equal(y2, y) and torch.equal(low2, low)
+
+
+def test_streams_and_graphs(cuda_lib):
+    tdr = cuda_lib
+    sets = [make(T, 512, 448, 6, 16, T, "runs") for T in (9, 200, 1500)]
+    ref = []
+    for i in sets:
+        s, (y, low, _) = call_forward(tdr, i)
+        ref.append((s, y, low, backward(tdr, s, i, low)))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for st, i in zip(streams, sets):
+            with torch.cuda.stream(st):
+                s, (y, low, _) = call_forward(tdr, i)
+                outs.append((y, low, backward(tdr, s, i, low)))
+    torch.cuda.synchronize()
+    for k, (y, low, grads) in enumerate(outs):
+        _, ry, rlow, rg = ref[k % 3]
+        assert torch.equal(y, ry) and torch.equal(low, rlow)
+        assert all(torch.equal(p, q) for p, q in zip(grads, rg))
+    ws = torch.empty(max(tdr.adapter_workspace_size(r[0]) for r in ref), dtype=torch.uint8,
+                     device="cuda")
+    graphs = []
+    for i in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s, (y, low, _) = call_forward(tdr, i, workspace=ws)
+            graphs.append((g, y, low, backward(tdr, s, i, low, workspace=ws)))
+    for _ in range(3):
+        for (g, y, low, grads), (_, ry, rlow, rg) in zip(graphs, ref):
+            g.replay()
+            assert torch.equal(y, ry) and torch.equal(low, rlow)
+            assert all(torch.equal(p, q) for p, q in zip(grads, rg))
+    assert tdr.device_status() == 0
+
+
+def test_gradients_against_differences(cuda_lib):
+    """<d, grad> against (f(v + h d) - f(v - h d)) / 2h of f = <y, d_y>, in 64 bits: f is linear in
+    x, A and B each, so the difference is exact but for the outputs' rounding of f itself; the
+    gradients are held to the bounds that their definition tests derive, summed over d."""
+    tdr = cuda_lib
+    T, d_in, d_out, L, r = 260, 192, 128, 3, 8
+    inp = make(T, d_in, d_out, L, r, 4)
+    s, (_, low, _) = call_forward(tdr, inp)
+    d_x, d_a, d_b = backward(tdr, s, inp, low)
+    v = {k: inp[k].double() for k in ("x", "w", "a", "b", "d_y")}
+
+    def f(x, a, b):
+        y = x @ v["w"]
+        for l in range(L):
+            t = (inp["ids"] == l).nonzero().squeeze(1)
+            y[t] += inp["scale"][l].double() * (x[t] @ a[l]) @ b[l]
+        return (y * v["d_y"]).sum()
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    for k, grad, rel in (("x", d_x, BF16), ("a", d_a, 2.0 ** -12), ("b", d_b, 2.0 ** -12)):
+        for _ in range(3):
+            d = torch.empty_like(v[k]).normal_(0, 1, generator=g)
+            at = dict(x=v["x"], a=v["a"], b=v["b"])
+            up, down = dict(at, **{k: v[k] + d}), dict(at, **{k: v[k] - d})
+            want = (f(**up) - f(**down)) / 2
+            got = (grad.double() * d).sum()
+            assert (got - want).abs() <= rel * (grad.double() * d).abs().sum() + 1e-9, k
+
+
+def test_rows_beyond_32_bit_offsets(cuda_lib):
+    tdr = cuda_lib
+    T, d_in, d_out, L, r = 540672, 4096, 64, 5, 8  # 2.2e9 values of x
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.empty(T, d_in, dtype=torch.bfloat16, device="cuda").normal_(0, 1, generator=g)
+    inp = make(2, d_in, d_out, L, r, 2)
+    inp["x"] = x
+    inp["ids"] = torch.randint(-1, L, (T,), generator=g, device="cuda").int()
+    inp["d_y"] = torch.empty(T, d_out, dtype=torch.bfloat16, device="cuda").normal_(0, 0.1, generator=g)
+    s, (y, low, _) = call_forward(tdr, inp)
+    d_x, d_a, d_b = backward(tdr, s, inp, low)
+    assert tdr.device_status() == 0
+    at = torch.cat([torch.arange(40), torch.arange(T // 2, T // 2 + 40), torch.arange(T - 300, T)]).cuda()
+    xs, ds, ids = x[at].double(), inp["d_y"][at].double(), inp["ids"][at]
+    w, a, b = (inp[k].double() for k in ("w", "a", "b"))
+    lref, lerr = low64(xs, a, ids, inp["scale"])
+    assert ((low[at].double() - lref).abs() <= lerr).all()
+    ref, err = through64(xs, w, lref, lerr, b, ids)
+    assert ((y[at].double() - ref).abs() <= err).all()
+    dl, dlerr = low64(ds, b.transpose(1, 2), ids, inp["scale"])
+    ref, err = through64(ds, w.t(), dl, dlerr, a.transpose(1, 2), ids)
+    assert ((d_x[at].double() - ref).abs() <= err).all()
+    for l in (0, L - 1):  # the sums over all rows, a slice of the columns
+        t = (inp["ids"] == l).nonzero().squeeze(1)
+        dy, xc = inp["d_y"][t].double(), x[t, -64:].double()
+        dl = inp["scale"][l].double() * (dy @ b[l].t())
+        n = t.numel() + 72
+        assert ((d_a[l, -64:].double() - xc.t() @ dl).abs() <= n * F32 * (xc.abs().t() @ dl.abs())).all()
+        lw = low[t].double()
+        assert ((d_b[l].double() - lw.t() @ dy).abs() <= n * F32 * (lw.abs().t() @ dy.abs())).all()
+
+
+def test_nothing_to_do_and_refusals(cuda_lib):
+    tdr = cuda_lib
+    inp = make(6, 128, 192, 3, 8, 1)
+    z = tdr.make_adapter_shape(0, 128, 192, 3, 8)
+    y, low, _ = tdr.adapter_forward(z, inp["x"][:0], inp["w"], inp["a"], inp["b"], inp["ids"][:0],
+                                    inp["scale"])
+    assert y.shape == (0, 192) and low.shape == (0, 8)
+    d_a = torch.ones(3, 128, 8, device="cuda")
+    _, d_a, d_b = tdr.adapter_backward(z, inp["d_y"][:0], inp["x"][:0], inp["w"], inp["a"], inp["b"],
+                                       inp["ids"][:0], inp["scale"], low, d_a=d_a)
+    assert (d_a == 0).all() and (d_b == 0).all()
+    s = tdr.make_adapter_shape(6, 128, 192, 3, 8)
+    names = ("x", "w", "a", "b", "ids", "scale")
+    for key, value in (("ids", inp["ids"].long()), ("scale", inp["scale"].double()),
+                       ("a", inp["a"].float()), ("b", inp["b"].transpose(1, 2)),
+                       ("w", inp["w"].cpu()), ("w", inp["w"].t()), ("x", inp["x"][:5])):
+        sick = dict(inp, **{key: value})
+        with pytest.raises((TypeError, ValueError)):
+            tdr.adapter_forward(s, *[sick[k] for k in names])
+        with pytest.raises((TypeError, ValueError)):
+            tdr.adapter_backward(s, inp["d_y"], *[sick[k] for k in names], low=torch.zeros_like(low))
+    _, (y, low, _) = call_forward(tdr, inp)
+    with pytest.raises((TypeError, ValueError)):
+        backward(tdr, s, inp, low.cpu())
+    with pytest.raises(ValueError):
+        backward(tdr, s, inp, low, d_x=torch.empty_like(inp["x"]), want_d_x=False)
+    with pytest.raises(tdr.MoEError):
+        call_forward(tdr, inp, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(tdr.MoEError):
+        backward(tdr, s, inp, low, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    for bad in (tdr.make_adapter_shape(6, 100, 192, 3, 8), tdr.make_adapter_shape(6, 128, 192, 3, 12),
+                tdr.make_adapter_shape(6, 128, 192, 3, 136), tdr.make_adapter_shape(6, 128, 192, 257, 8),
+                tdr.make_adapter_shape(6, 128, 192, 3, 8, torch.float32)):
+        with pytest.raises(tdr.MoEError):
+            tdr.adapter_forward(bad, *[inp[k] for k in names])
+    assert tdr.device_status() == 0
+
+
+def test_a_decode_step_and_a_tuning_step(cuda_lib):
+    """The calls as a program makes them: projection with adapters, then the layer; and the
+    gradient of a loss through the layer into the adapters."""
+    tdr = cuda_lib
+    T, d, L, r, E, K, n = 48, 512, 5, 16, 16, 4, 384
+    inp = make(T, 256, d, L, r, 3)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+
+    def normal(*shape, std):
+        return torch.empty(*shape, dtype=torch.bfloat16, device="cuda").normal_(0, std, generator=g)
+
+    w_r, wg, wu = normal(d, E, std=0.05), normal(E, d, n, std=0.05), normal(E, d, n, std=0.05)
+    wd = normal(E, n, d, std=0.05)
+    s, (h, low, _) = call_forward(tdr, inp)
+    layer = tdr.make_shape(T, d, E, K, n)
+    out, _ = tdr.decode(layer, h, w_r, wg, wu, wd)
+    full, ws, pre = tdr.forward_h(layer, h, w_r, wg, wu, wd)
+    # two expert outputs' roundings apart, of the size of the row
+    assert ((out.float() - full.float()).norm() / full.float().norm()) < 2 ** -6
+    # captured: the same values on replay
+    graph = torch.cuda.CUDAGraph()
+    a_ws = torch.empty(tdr.adapter_workspace_size(s), dtype=torch.uint8, device="cuda")
+    d_ws = torch.empty(tdr.decode_workspace_size(layer), dtype=torch.uint8, device="cuda")
+    with torch.cuda.graph(graph):
+        h2, _, _ = call_forward(tdr, inp, workspace=a_ws)[1]
+        out2, _ = tdr.decode(layer, h2, w_r, wg, wu, wd, workspace=d_ws)
+    graph.replay()
+    assert torch.equal(out2, out)
+    # tuning: d_out -> layer -> projection
+    v = tdr.workspace_views(layer, ws)
+    d_out = normal(T, d, std=0.1)
+    d_h, d_w, d_in = tdr.backward(layer, d_out, v["topk_w"], v["offsets"], v["perm_to_assign"],
+                                  v["assign_to_perm"], wd, pre, wg, wu, input_grad=True)
+    tdr.backward_router(layer, h, w_r, v["topk_ids"], v["topk_w"], d_w, d_x=d_in)
+    d_x, d_a, d_b = backward(tdr, s, dict(inp, d_y=d_in), low)
+    assert tdr.device_status() == 0
+    # autograd of the same chain in 64 bits, the layer's selection held fixed
+    x, a, b = (inp[k].double().requires_grad_() for k in ("x", "a", "b"))
+    parts = [x @ inp["w"].double()]
+    for l in range(L):
+        own = (inp["ids"] == l).double().unsqueeze(1)
+        parts.append(own * inp["scale"][l].double() * ((x @ a[l]) @ b[l]))
+    hh = sum(parts)
+    ids = v["topk_ids"].long()
+    wt = torch.softmax((hh @ w_r.double()).gather(1, ids), 1)
+    y = torch.zeros_like(hh)
+    for e in range(E):
+        up, gate = hh @ wu[e].double(), hh @ wg[e].double()
+        ye = (torch.nn.functional.silu(gate) * up) @ wd[e].double()
+        y = y + ((ids == e) * wt).sum(1, keepdim=True) * ye
+    (y * d_out.double()).sum().backward()
+    for got, want in ((d_x, x.grad), (d_a, a.grad), (d_b, b.grad)):
+        # bf16 roundings of h, the activations and the layer's input gradient: a few 2^-8
+        assert ((got.double() - want).norm() / want.norm()) < 6 * BF16

@@ -407,7 +407,7 @@ moe_status run(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& 
 // partials a second kernel adds in order. (2880 x 2880, 2049 rows: 108 tiles on 74 pairs took two
 // rounds.) Returns the number of partials.
 int adapter_gemm_split(int T, int k_dim, int n_out, int* whole, int* split) {
-  const int pairs = sm_count() / 2;
+  const int pairs = sm_count() > 1 ? sm_count() / 2 : 1;  // a host without a device counts one SM
   const int tiles = ((T + PAIR_M - 1) / PAIR_M) * ((n_out + BN - 1) / BN);
   const int rest = tiles % pairs;
   int s = rest > 0 ? pairs / rest : 1;
