@@ -6,13 +6,15 @@
 // gathered by cp.async into the swizzled layout that the tensor cores read; both operands are
 // taken as they lie (a row is one k of the product: MN-major), so nothing is transposed. M is
 // the wide side (256 columns a unit, two accumulators), N the rank (16 ... 128), K the rows.
-// The low-rank side is fp32: it enters as three bf16 terms accumulated one after another, exact
-// to 2^-24, so the fp32 gradients lose nothing; the tensor pipe has the time (three MMAs of
-// N = r for each 32 x 256 tile of wide rows).
+// The low-rank side is fp32: it enters as three bf16 terms, exact to 2^-24; the tensor pipe has
+// the time (three MMAs of N = r for each 32 x 256 tile of wide rows). The tensor core cuts what
+// it adds to an accumulator off rather than rounding it, an error that grows with the number of
+// additions: the small second and third terms have an accumulator of their own, added to the
+// first's at the end (512 rows, relative to the gradient: 1.7e-6 in one accumulator, 0.5e-6 in two).
 //
 // A unit is (adapter, chunk of its rows, 256 columns of x or of d_y). Two CTAs an SM run through
-// the units, each with two pairs of accumulators, so that loads run on while a unit is stored
-// (many adapters have only a few rows each). Chunks of one adapter leave partial sums that a
+// the units; up to rank 32 TMEM holds the accumulators of two units for each, so that the
+// products of the next run beside the stores of the last (many adapters have only a few rows). Chunks of one adapter leave partial sums that a
 // second kernel adds in chunk order (results repeat bit for bit); it is launched only where an
 // adapter can have two chunks. An adapter without rows has one empty chunk, which writes zeros.
 // Every wait is bounded (MOE_ERR_TIMEOUT on expiry).
@@ -44,6 +46,7 @@ struct OuterArgs {
   int T, r, L, chunk;
   int n_mma;          // the rank rounded up to 16
   int nc;             // its 64-column pieces
+  int bufs;           // units whose accumulators TMEM holds: 1 or 2
   unsigned* status;
   unsigned long long limit_ns;
 };
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(THREADS)
   const uint32_t sb = (saddr(smem_raw) + 1023u) & ~1023u;
   const int p_bytes = g.nc * CHUNK, st_bytes = BIG_BYTES + 3 * p_bytes;
   volatile int* abort_flag = &s_abort;
-  const uint32_t tcols = tmem_columns(4 * g.n_mma);
+  const uint32_t tcols = tmem_columns(g.bufs * 4 * g.n_mma);
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -247,12 +250,12 @@ __global__ void __launch_bounds__(THREADS)
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += step, ++it) {
       const Unit v = unit_of(u, table, g);
-      const int steps = (v.n + OT - 1) / OT, buf = it & 1;
-      if (!mbar_wait_warp(saddr(&tempty[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag,
-                          g.status, limit))
+      const int steps = (v.n + OT - 1) / OT, buf = it & (g.bufs - 1);
+      if (!mbar_wait_warp(saddr(&tempty[buf]), ((uint32_t)(it >> (g.bufs - 1)) & 1u) ^ 1u,
+                          abort_flag, g.status, limit))
         break;
       tc_fence_after();
-      const uint32_t acc = tmem + (uint32_t)(buf * 2 * g.n_mma);
+      const uint32_t acc = tmem + (uint32_t)(buf * 4 * g.n_mma);
       for (int s = 0; s < steps; ++s) {
         if (!mbar_wait_warp(saddr(&full[stage]), phase, abort_flag, g.status, limit)) {
           ok = false;
@@ -268,10 +271,10 @@ __global__ void __launch_bounds__(THREADS)
             for (int kk = 0; kk < OT / 16; ++kk)
 #pragma unroll
               for (int m = 0; m < 2; ++m)
-                tc_mma<1>(acc + (uint32_t)(m * g.n_mma),
+                tc_mma<1>(acc + (uint32_t)(((q > 0 ? 2 : 0) + m) * g.n_mma),
                           bd0 + so + (uint64_t)((m * 2 * CHUNK + kk * 2048) >> 4),
                           pd0 + so + (uint64_t)((q * p_bytes + kk * 2048) >> 4), idesc,
-                          (s > 0 || q > 0 || kk > 0) ? 1u : 0u);
+                          (s > 0 || q > 1 || kk > 0) ? 1u : 0u);
           tc_commit<1>(saddr(&empty[stage]));
         }
         __syncwarp();
@@ -297,23 +300,27 @@ __global__ void __launch_bounds__(THREADS)
     int it = 0;
     for (int u = blockIdx.x; u < units; u += step, ++it) {
       const Unit v = unit_of(u, table, g);
-      const int buf = it & 1, D = g.D[v.p];
+      const int buf = it & (g.bufs - 1), D = g.D[v.p];
       float* dst = v.slot < 0 ? g.out[v.p] + (size_t)v.l * D * g.r
                               : g.part + (size_t)v.slot * wide + (v.p ? (size_t)g.D[0] * g.r : 0);
-      if (!mbar_wait_warp(saddr(&tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, g.status,
-                          limit))
+      if (!mbar_wait_warp(saddr(&tfull[buf]), (uint32_t)(it >> (g.bufs - 1)) & 1u, abort_flag,
+                          g.status, limit))
         break;
       tc_fence_after();
-      const uint32_t acc = tmem + (uint32_t)(buf * 2 * g.n_mma) + ((uint32_t)(q * 32) << 16);
+      const uint32_t acc = tmem + (uint32_t)(buf * 4 * g.n_mma) + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
       for (int m = 0; m < 2; ++m) {
         const int c = v.c0 + m * 128 + q * 32 + lane;
 #pragma unroll 2
         for (int j0 = 0; j0 < g.r; j0 += 8) {
-          uint32_t f[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+          uint32_t f[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, f2[8];
           if (v.n > 0) {  // else no rows: zeros
             tmem_ld8(acc + (uint32_t)(m * g.n_mma + j0), f);
+            tmem_ld8(acc + (uint32_t)((2 + m) * g.n_mma + j0), f2);
             tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              f[j] = __float_as_uint(__uint_as_float(f[j]) + __uint_as_float(f2[j]));
           }
           if (c >= D) continue;
           if (v.p == 0) {
@@ -428,6 +435,7 @@ moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const 
   a.chunk = chunk_of(T, d_in, d_out);
   a.n_mma = (r + 15) / 16 * 16;
   a.nc = (r + 63) / 64;
+  a.bufs = a.n_mma <= 32 ? 2 : 1;
   a.status = device_status_ptr();
   a.limit_ns = kWaitLimitNs;
   const int smem = 1024 + STAGES * (BIG_BYTES + 3 * a.nc * CHUNK);
@@ -440,7 +448,7 @@ moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const 
   if (!make_map(&m0, planes_d_low, 3, pd, ps, pbox) || !make_map(&m1, planes_low, 3, pd, ps, pbox))
     return MOE_ERR_CUDA;
   launch_begin(K_ADAPTER_OUTER, st);
-  // two CTAs an SM (one for a rank above 64, whose accumulators take all of TMEM)
+  // two CTAs an SM, of 256 TMEM columns each (one for a rank above 64, which takes all 512)
   const long long most = (long long)(T / a.chunk + L) * (a.tiles[0] + a.tiles[1]);
   const int ctas = (a.nc == 1 ? 2 : 1) * sm_count();
   launch_kernel(adapter_outer_kernel, dim3((unsigned)(most < ctas ? most : ctas)), dim3(THREADS),
