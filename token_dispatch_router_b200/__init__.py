@@ -154,11 +154,12 @@ def make_shape(T: int, d: int, E: int, K: int, n: int = 0, capacity_factor: floa
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream() -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _stream() -> int:
+    # the handle alone: torch.cuda.current_stream() makes a stream object first, 3 us of a call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> None:
@@ -174,6 +175,8 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> None:
 
 def _current(t: torch.Tensor, name: str) -> torch.device:
     """The device of `t`, which has to be the current one (the library launches there)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     if t.device.index != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
@@ -181,6 +184,8 @@ def _current(t: torch.Tensor, name: str) -> torch.device:
 
 
 def _on(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return  # as it has to be; what is wrong is looked for below
     _dev(t, name, dtype, shape)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
@@ -419,28 +424,30 @@ def decode(shape: moe_shape, x, w_r, w_gate, w_up, w_down, bias=None, logits_in=
     Returns (out [T, d], workspace)."""
     lib = load_library()
     T, d, E, n = shape.T, shape.d, shape.E, shape.n
-    need = decode_workspace_size(shape)
-    if need == 0:
-        raise MoEError(lib.moe_decode(ctypes.byref(shape), *[None] * 9, 0, None), "moe_decode")
-    _dev(x, "x", torch.bfloat16, (T, d))
+    bf = torch.bfloat16
+    if workspace is None:  # a given one is measured by the call
+        need = decode_workspace_size(shape)
+        if need == 0:
+            raise MoEError(lib.moe_decode(ctypes.byref(shape), *[None] * 9, 0, None), "moe_decode")
+    _on(x, "x", bf, (T, d), x.device)
     dev = _current(x, "x")
     if logits_in is None:
-        _on(w_r, "w_r", torch.bfloat16, (d, E), dev)
+        _on(w_r, "w_r", bf, (d, E), dev)
     else:
         _on(logits_in, "logits_in", torch.float32, (T, E), dev)
-    _on(w_gate, "w_gate", torch.bfloat16, (E, d, n), dev)
-    _on(w_up, "w_up", torch.bfloat16, (E, d, n), dev)
-    _on(w_down, "w_down", torch.bfloat16, (E, n, d), dev)
+    _on(w_gate, "w_gate", bf, (E, d, n), dev)
+    _on(w_up, "w_up", bf, (E, d, n), dev)
+    _on(w_down, "w_down", bf, (E, n, d), dev)
     if bias is not None:
         _on(bias, "bias", torch.float32, (E,), dev)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
-        _on(workspace, "workspace", torch.uint8, None, dev)
+        _on(workspace, "workspace", torch.uint8, workspace.shape, dev)
     if out is None:
-        out = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(T, d, dtype=bf, device=dev)
     else:
-        _on(out, "out", torch.bfloat16, (T, d), dev)
+        _on(out, "out", bf, (T, d), dev)
     _check(lib.moe_decode(ctypes.byref(shape), _ptr(x), _ptr(w_r), _ptr(bias), _ptr(logits_in),
                           _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out), _ptr(workspace),
                           workspace.numel(), _stream()), "moe_decode")
@@ -458,28 +465,32 @@ def adapter_workspace_size(shape: moe_adapter_shape) -> int:
     return int(load_library().moe_adapter_workspace_size(ctypes.byref(shape)))
 
 
-def _adapter_workspace(shape: moe_adapter_shape, workspace, dev):
+def _adapter_need(shape: moe_adapter_shape, workspace, where: str) -> int:
+    """Bytes of a workspace to make (0 where one was given, which the call measures)."""
+    if workspace is not None:
+        return 0
     need = adapter_workspace_size(shape)
+    if need == 0:
+        lib = load_library()
+        raise MoEError(lib.moe_adapter_forward(ctypes.byref(shape), *[None] * 9, 0, None), where)
+    return need
+
+
+def _adapter_workspace(need: int, workspace, dev):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev)
-    _on(workspace, "workspace", torch.uint8, None, dev)
+    _on(workspace, "workspace", torch.uint8, workspace.shape, dev)
     return workspace
-
-
-def _check_adapter_shape(shape: moe_adapter_shape, where: str) -> None:
-    lib = load_library()
-    if lib.moe_adapter_workspace_size(ctypes.byref(shape)) == 0:
-        raise MoEError(lib.moe_adapter_forward(ctypes.byref(shape), *[None] * 9, 0, None), where)
 
 
 def adapter_forward(shape: moe_adapter_shape, x, w, a, b, ids, scale, low=None, out=None,
                     workspace=None):
     """moe_adapter_forward: x W + scale[l] (x A[l]) B[l] with l = ids[row], -1 for none.
     Returns (y [T, d_out] bf16, low [T, rank] fp32, workspace); the backward reads low."""
-    _check_adapter_shape(shape, "moe_adapter_forward")
+    need = _adapter_need(shape, workspace, "moe_adapter_forward")
     T, d_in, d_out, L, r = (shape.T, shape.d_in, shape.d_out, shape.n_adapters, shape.rank)
     bf = torch.bfloat16
-    _dev(x, "x", bf, (T, d_in))
+    _on(x, "x", bf, (T, d_in), x.device)
     dev = _current(x, "x")
     _on(w, "w", bf, (d_in, d_out), dev)
     _on(a, "a", bf, (L, d_in, r), dev)
@@ -494,7 +505,7 @@ def adapter_forward(shape: moe_adapter_shape, x, w, a, b, ids, scale, low=None, 
         out = torch.empty(T, d_out, dtype=bf, device=dev)
     else:
         _on(out, "out", bf, (T, d_out), dev)
-    workspace = _adapter_workspace(shape, workspace, dev)
+    workspace = _adapter_workspace(need, workspace, dev)
     _check(load_library().moe_adapter_forward(
         ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(a), _ptr(b), _ptr(ids), _ptr(scale),
         _ptr(low), _ptr(out), _ptr(workspace), workspace.numel(), _stream()),
@@ -506,10 +517,10 @@ def adapter_backward(shape: moe_adapter_shape, d_y, x, w, a, b, ids, scale, low,
                      d_a=None, d_b=None, want_d_x: bool = True, workspace=None):
     """moe_adapter_backward (w held fixed); low from adapter_forward on the same arguments.
     Returns (d_x [T, d_in] bf16 or None, d_a [L, d_in, r] fp32, d_b [L, r, d_out] fp32)."""
-    _check_adapter_shape(shape, "moe_adapter_backward")
+    need = _adapter_need(shape, workspace, "moe_adapter_backward")
     T, d_in, d_out, L, r = (shape.T, shape.d_in, shape.d_out, shape.n_adapters, shape.rank)
     bf, f32 = torch.bfloat16, torch.float32
-    _dev(d_y, "d_y", bf, (T, d_out))
+    _on(d_y, "d_y", bf, (T, d_out), d_y.device)
     dev = _current(d_y, "d_y")
     _on(x, "x", bf, (T, d_in), dev)
     if want_d_x:
@@ -533,7 +544,7 @@ def adapter_backward(shape: moe_adapter_shape, d_y, x, w, a, b, ids, scale, low,
         d_b = torch.empty(L, r, d_out, dtype=f32, device=dev)
     else:
         _on(d_b, "d_b", f32, (L, r, d_out), dev)
-    workspace = _adapter_workspace(shape, workspace, dev)
+    workspace = _adapter_workspace(need, workspace, dev)
     _check(load_library().moe_adapter_backward(
         ctypes.byref(shape), _ptr(d_y), _ptr(x), _ptr(w if want_d_x else None), _ptr(a), _ptr(b),
         _ptr(ids), _ptr(scale), _ptr(low), _ptr(d_x), _ptr(d_a), _ptr(d_b), _ptr(workspace),
