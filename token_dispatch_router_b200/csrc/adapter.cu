@@ -30,13 +30,18 @@ moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapt
                                const void* in, const void* w, const AdapterTile* tiles,
                                const void* low, const void* m, void* out, float* part,
                                cudaStream_t st);
+moe_status launch_adapter_gemm_sum(int T, int k_dim, int n_out, void* out, float* part,
+                                   cudaStream_t st);
 size_t adapter_gemm_part_bytes(int T, int k_dim, int n_out);
-size_t adapter_outer_part_bytes(int T, int d_in, int d_out, int r);
+size_t adapter_outer_part_bytes(int T, int r);
 moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
                                 const void* d_y, const void* planes_d_low,
                                 const void* planes_low, const int32_t* offsets,
                                 const int32_t* rows, float* d_a, float* d_b, float* part,
-                                cudaStream_t st);
+                                bool early, cudaStream_t st);
+moe_status launch_adapter_outer_sum(int T, int d_in, int d_out, int r, int L,
+                                    const int32_t* offsets, float* d_a, float* d_b, float* part,
+                                    cudaStream_t st);
 
 namespace {
 
@@ -87,7 +92,7 @@ Layout layout(const moe_adapter_shape& s) {
   L.d_low = take(T * r * 4);
   L.planes_d = take(3 * T * r * 2);
   L.planes_l = take(3 * T * r * 2);
-  L.part = take(adapter_outer_part_bytes(s.T, s.d_in, s.d_out, s.rank));
+  L.part = take(adapter_outer_part_bytes(s.T, s.rank));
   L.total = o;
   return L;
 }
@@ -137,9 +142,12 @@ moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, con
                               scale, low, nullptr, nullptr, nullptr, ws + L.terms,
                               (AdapterTile*)(ws + L.tiles), st)) != MOE_OK)
     return r;
-  return launch_adapter_gemm(false, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w,
-                             (const AdapterTile*)(ws + L.tiles), ws + L.terms, b, y,
-                             (float*)(ws + L.gemm_part), st);
+  float* part = (float*)(ws + L.gemm_part);
+  if ((r = launch_adapter_gemm(false, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w,
+                               (const AdapterTile*)(ws + L.tiles), ws + L.terms, b, y, part,
+                               st)) != MOE_OK)
+    return r;
+  return launch_adapter_gemm_sum(s.T, s.d_in, s.d_out, y, part, st);
 }
 
 moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, const void* x,
@@ -158,14 +166,23 @@ moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, 
            ws + L.planes_d, low, ws + L.planes_l, ws + L.terms, (AdapterTile*)(ws + L.tiles),
            st)) != MOE_OK)
     return r;
+  float* gemm_part = (float*)(ws + L.gemm_part);
+  float* part = (float*)(ws + L.part);
   if (d_x != nullptr &&
       (r = launch_adapter_gemm(true, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, d_y, w,
                                (const AdapterTile*)(ws + L.tiles), ws + L.terms, a, d_x,
-                               (float*)(ws + L.gemm_part), st)) != MOE_OK)
+                               gemm_part, st)) != MOE_OK)
     return r;
-  return launch_adapter_outer(s.T, s.d_in, s.d_out, s.rank, s.n_adapters, x, d_y,
-                              ws + L.planes_d, ws + L.planes_l, offsets, rows, d_a, d_b,
-                              (float*)(ws + L.part), st);
+  // the outer products start as the large product's CTAs leave; both sums come behind them
+  if ((r = launch_adapter_outer(s.T, s.d_in, s.d_out, s.rank, s.n_adapters, x, d_y,
+                                ws + L.planes_d, ws + L.planes_l, offsets, rows, d_a, d_b, part,
+                                d_x != nullptr, st)) != MOE_OK)
+    return r;
+  if (d_x != nullptr && (r = launch_adapter_gemm_sum(s.T, s.d_out, s.d_in, d_x, gemm_part, st)) !=
+                            MOE_OK)
+    return r;
+  return launch_adapter_outer_sum(s.T, s.d_in, s.d_out, s.rank, s.n_adapters, offsets, d_a, d_b,
+                                  part, st);
 }
 
 }  // namespace moe

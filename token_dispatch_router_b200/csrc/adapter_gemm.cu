@@ -391,13 +391,7 @@ moe_status run(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& 
   launch_begin(K_ADAPTER_GEMM, st);
   launch_kernel(kern, dim3((unsigned)(2 * pairs)), dim3(THREADS), (size_t)SMEM_BYTES, st, 2, ma,
                 mb, ml, mm, a);
-  const moe_status s = launch_end(K_ADAPTER_GEMM, st);
-  if (s != MOE_OK || a.split == 1) return s;
-  launch_begin(K_ADAPTER_GEMM_SUM, st);
-  launch_kernel(adapter_gemm_sum_kernel,
-                dim3(PAIR_M * BN / 8 / SUM_THREADS, (unsigned)(a.mt * a.nt - a.whole)),
-                dim3(SUM_THREADS), 0, st, 1, a);
-  return launch_end(K_ADAPTER_GEMM_SUM, st);
+  return launch_end(K_ADAPTER_GEMM, st);
 }
 
 }  // namespace
@@ -430,22 +424,29 @@ size_t adapter_gemm_part_bytes(int T, int k_dim, int n_out) {
 
 // in [T, k_dim], w [d_in, d_out]; forward: k_dim = d_in, out [T, d_out], m = B; backward:
 // k_dim = d_out, out [T, d_in], m = A. low: [2][T][rank] bf16 terms.
-moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
-                               const void* in, const void* w, const AdapterTile* tiles,
-                               const void* low, const void* m, void* out, float* part,
-                               cudaStream_t st) {
+namespace {
+AdapterGemmArgs gemm_args(int T, int k_dim, int n_out, void* out, float* part) {
   AdapterGemmArgs a = {};
-  const int k_dim = bwd ? d_out : d_in, n_out = bwd ? d_in : d_out;
   a.T = T;
   a.n_out = n_out;
   a.kblocks = k_dim / BK;
   a.mt = (T + PAIR_M - 1) / PAIR_M;
   a.nt = (n_out + BN - 1) / BN;
-  a.rank = rank;
   adapter_gemm_split(T, k_dim, n_out, &a.whole, &a.split);
   a.part = part;
-  a.tiles = tiles;
   a.out = (bf16*)out;
+  return a;
+}
+}  // namespace
+
+moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
+                               const void* in, const void* w, const AdapterTile* tiles,
+                               const void* low, const void* m, void* out, float* part,
+                               cudaStream_t st) {
+  const int k_dim = bwd ? d_out : d_in, n_out = bwd ? d_in : d_out;
+  AdapterGemmArgs a = gemm_args(T, k_dim, n_out, out, part);
+  a.rank = rank;
+  a.tiles = tiles;
   a.status = device_status_ptr();
   a.limit_ns = kWaitLimitNs;
   CUtensorMap ma, mb, ml, mm;
@@ -462,6 +463,18 @@ moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapt
       !make_map(&ml, low, 3, ld, ls, lbox) || !make_map(&mm, m, 3, md, ms, mbox))
     return MOE_ERR_CUDA;
   return bwd ? run<true>(ma, mb, ml, mm, a, st) : run<false>(ma, mb, ml, mm, a, st);
+}
+
+// After launch_adapter_gemm (and whatever may come between): the tiles that were split.
+moe_status launch_adapter_gemm_sum(int T, int k_dim, int n_out, void* out, float* part,
+                                   cudaStream_t st) {
+  const AdapterGemmArgs a = gemm_args(T, k_dim, n_out, out, part);
+  if (a.split == 1) return MOE_OK;
+  launch_begin(K_ADAPTER_GEMM_SUM, st);
+  launch_kernel(adapter_gemm_sum_kernel,
+                dim3(PAIR_M * BN / 8 / SUM_THREADS, (unsigned)(a.mt * a.nt - a.whole)),
+                dim3(SUM_THREADS), 0, st, 1, a);
+  return launch_end(K_ADAPTER_GEMM_SUM, st);
 }
 
 }  // namespace moe

@@ -12,13 +12,19 @@
 // additions: the small second and third terms have an accumulator of their own, added to the
 // first's at the end (512 rows, relative to the gradient: 1.7e-6 in one accumulator, 0.5e-6 in two).
 //
-// A unit is (adapter, chunk of its rows, 256 columns of x or of d_y). Two CTAs an SM run through
-// the units; up to rank 32 TMEM holds the accumulators of two units for each, so that the
-// products of the next run beside the stores of the last (many adapters have only a few rows). Chunks of one adapter leave partial sums that a
-// second kernel adds in chunk order (results repeat bit for bit); it is launched only where an
-// adapter can have two chunks. An adapter without rows has one empty chunk, which writes zeros.
+// A unit is (adapter, 256 columns of x or of d_y). The units' row steps lie on a line, each unit
+// with a few positions more for its stores, and the line is cut into equal pieces, one a CTA, two
+// CTAs an SM: adapters have any number of rows (8192 rows of 8 adapters, 4096 + 4096 columns, in
+// turn over chunks of 512 rows: LATER us, in equal pieces LATER). Units that a cut goes through leave
+// partial sums, at most two a CTA, that a second kernel adds in order (results repeat bit for
+// bit). Up to 512 rows units stay whole, and the second kernel is not launched. An adapter without
+// rows writes zeros. Up to rank 32 TMEM holds the accumulators of two units, so that the products
+// of the next run beside the stores of the last.
+//
+// After the large product the kernel starts as that one's CTAs leave: it reads nothing of it.
 // Every wait is bounded (MOE_ERR_TIMEOUT on expiry).
 #include "adapter.cuh"
+#include "few.cuh"
 #include "ffn_args.cuh"
 
 namespace moe {
@@ -34,6 +40,8 @@ constexpr int STAGES = 3;
 constexpr int CHUNK = OT * 128;              // OT rows x 64 columns
 constexpr int BIG_BYTES = OC / 64 * CHUNK;   // 16 KB
 constexpr int kMaxAdapters = 256;
+constexpr int CHAIN = 32;    // steps in one accumulator; a longer unit's sums are added in fp32
+constexpr int WHOLE_ROWS = 512;  // up to here units are not cut
 
 struct OuterArgs {
   const bf16* big[2];     // x [T, D0], d_y [T, D1]
@@ -42,8 +50,11 @@ struct OuterArgs {
   int D[2], tiles[2];     // widths and their 256-column tiles
   const int32_t* offsets;
   const int32_t* rows;
-  float* part;        // [chunk][(D0 + D1) r]: adapters of several chunks
-  int T, r, L, chunk;
+  float* part;        // [2 CTAs][256 r]: the units that a piece begins and ends inside
+  int T, r, L;
+  int ctas, cut;      // pieces at most; whether a piece may end inside a unit
+  int store;          // positions of a unit's stores
+  int early;          // the previous kernel is none that this one reads from
   int n_mma;          // the rank rounded up to 16
   int nc;             // its 64-column pieces
   int bufs;           // units whose accumulators TMEM holds: 1 or 2
@@ -51,58 +62,76 @@ struct OuterArgs {
   unsigned long long limit_ns;
 };
 
-struct Table {
-  int chunk0[kMaxAdapters + 1];  // first chunk of each adapter
-  int multi0[kMaxAdapters];      // its first place among the chunks that leave partials
+// The line: first position of each adapter (`base`), whose units, one a column tile, have
+// steps + store positions each.
+struct Line {
+  int base[kMaxAdapters + 1];
 };
-struct Unit {
-  int l, p, c0, lo, n, slot;  // adapter, side, first column, first slot, rows; partial (-1: whole)
-};
-
-__device__ __forceinline__ void make_table(Table& t, const OuterArgs& g) {  // one warp
-  const int lane = threadIdx.x & 31;
-  int run = 0, mrun = 0;
+__device__ __forceinline__ int steps_of(int l, const OuterArgs& g) {
+  return (g.offsets[l + 1] - g.offsets[l] + OT - 1) / OT;
+}
+__device__ __forceinline__ void make_line(Line& t, const OuterArgs& g) {  // one warp
+  const int lane = threadIdx.x & 31, nct = g.tiles[0] + g.tiles[1];
+  int run = 0;
   for (int l0 = 0; l0 < g.L; l0 += 32) {
-    const int l = l0 + lane;
-    const int c = l < g.L ? g.offsets[l + 1] - g.offsets[l] : 0;
-    const int n = l < g.L ? max(1, (c + g.chunk - 1) / g.chunk) : 0, m = n > 1 ? n : 0;
-    int incl = n, mincl = m;
+    const int l = l0 + lane, n = l < g.L ? (steps_of(l, g) + g.store) * nct : 0;
+    int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      const int w = __shfl_up_sync(0xffffffffu, mincl, o);
-      if (lane >= o) {
-        incl += v;
-        mincl += w;
-      }
+      if (lane >= o) incl += v;
     }
-    if (l < g.L) {
-      t.chunk0[l] = run + incl - n;
-      t.multi0[l] = mrun + mincl - m;
-    }
+    if (l < g.L) t.base[l] = run + incl - n;
     run += __shfl_sync(0xffffffffu, incl, 31);
-    mrun += __shfl_sync(0xffffffffu, mincl, 31);
   }
-  if (lane == 0) t.chunk0[g.L] = run;
+  if (lane == 0) t.base[g.L] = run;
 }
-__device__ __forceinline__ Unit unit_of(int u, const Table& t, const OuterArgs& g) {
-  const int nct = g.tiles[0] + g.tiles[1], cg = u / nct, ct = u % nct;
-  int lo = 0, hi = g.L - 1;  // the last adapter whose chunks begin at cg or before
+__device__ __forceinline__ int adapter_at(int pos, const Line& t, int L) {
+  int lo = 0, hi = L - 1;  // the last adapter that begins at pos or before
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (t.chunk0[mid] <= cg) lo = mid;
+    if (t.base[mid] <= pos) lo = mid;
     else hi = mid - 1;
   }
-  Unit v;
-  v.l = lo;
-  const int i = cg - t.chunk0[lo], first = g.offsets[lo] + i * g.chunk;
-  v.p = ct >= g.tiles[0] ? 1 : 0;
-  v.c0 = (ct - (v.p ? g.tiles[0] : 0)) * OC;
-  v.lo = first;
-  v.n = max(0, min(g.chunk, g.offsets[lo + 1] - first));
-  v.slot = t.chunk0[lo + 1] - t.chunk0[lo] > 1 ? t.multi0[lo] + i : -1;
-  return v;
+  return lo;
 }
+__device__ __forceinline__ FewPieces pieces_of(const Line& t, const OuterArgs& g) {
+  return FewPieces(t.base[g.L], 4, g.ctas);
+}
+
+// The parts of units in this CTA's piece, one after another.
+struct Walk {
+  int pos, end;                  // of the piece, still to come
+  int l, p, c0, lo, n, s0, s1;   // adapter, side, first column; the adapter's first slot and rows; steps
+  int slot;                      // place of the partial, -1 where the unit is whole
+  __device__ __forceinline__ Walk(const Line& t, const OuterArgs& g) {
+    const FewPieces pc = pieces_of(t, g);
+    const int c = blockIdx.x;
+    pos = c < pc.n ? pc.begin(c) : 0;
+    end = c < pc.n ? pc.begin(c + 1) : 0;
+    l = pos < end ? adapter_at(pos, t, g.L) : 0;
+  }
+  __device__ __forceinline__ bool next(const Line& t, const OuterArgs& g) {
+    while (pos < end) {
+      while (t.base[l + 1] <= pos) ++l;
+      lo = g.offsets[l];
+      n = g.offsets[l + 1] - lo;
+      const int steps = (n + OT - 1) / OT, w = steps + g.store;
+      const int ct = (pos - t.base[l]) / w, u0 = t.base[l] + ct * w;
+      const int a = pos - u0, b = g.cut ? min(end - u0, w) : w;
+      pos = u0 + b;
+      s0 = a;
+      s1 = min(b, steps);
+      // a unit that is not cut belongs to the piece that holds its first position
+      if (steps == 0 || !g.cut ? a > 0 : s0 >= s1) continue;
+      p = ct >= g.tiles[0] ? 1 : 0;
+      c0 = (ct - (p ? g.tiles[0] : 0)) * OC;
+      slot = s0 > 0 ? 2 * (int)blockIdx.x : s1 < steps ? 2 * (int)blockIdx.x + 1 : -1;
+      return true;
+    }
+    return false;
+  }
+};
 
 __global__ void __launch_bounds__(THREADS)
     adapter_outer_kernel(const __grid_constant__ CUtensorMap tmP0,
@@ -111,7 +140,7 @@ __global__ void __launch_bounds__(THREADS)
   __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ Table table;
+  __shared__ Line line;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sb = (saddr(smem_raw) + 1023u) & ~1023u;
   const int p_bytes = g.nc * CHUNK, st_bytes = BIG_BYTES + 3 * p_bytes;
@@ -136,15 +165,16 @@ __global__ void __launch_bounds__(THREADS)
     prefetch_map(&tmP0);
     prefetch_map(&tmP1);
   }
-  pdl_wait();  // the previous kernel in the stream has completed
+  // early: the large product before this kernel waited for what both read, and wrote none of it
+  if (!g.early) pdl_wait();  // the previous kernel in the stream has completed
   pdl_trigger();
-  if (warp == 0) make_table(table, g);
+  if (warp == 0) make_line(line, g);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const uint64_t limit = g.limit_ns;
-  const int units = table.chunk0[g.L] * (g.tiles[0] + g.tiles[1]), step = (int)gridDim.x;
+  Walk v(line, g);
 
   if (warp < 4) {
     // ------------------------------------------------------------ gather
@@ -154,9 +184,8 @@ __global__ void __launch_bounds__(THREADS)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += step) {
-      const Unit v = unit_of(u, table, g);
-      const int steps = (v.n + OT - 1) / OT, D = g.D[v.p];
+    while (ok && v.next(line, g)) {
+      const int D = g.D[v.p];
       const bf16* big = g.big[v.p] + v.c0 + lane * 8;
       const bool col_on = v.c0 + lane * 8 < D;
       // lane i < 8 holds the row of this warp's i-th row in the next stage
@@ -164,10 +193,10 @@ __global__ void __launch_bounds__(THREADS)
         const int r = s * OT + warp + 4 * (lane & 7);
         return r < v.n ? g.rows[v.lo + r] : -1;
       };
-      int ahead = steps > 0 ? row_of(0) : -1;
-      for (int s = 0; s < steps; ++s) {
+      int ahead = v.s0 < v.s1 ? row_of(v.s0) : -1;
+      for (int s = v.s0; s < v.s1; ++s) {
         const int mine = ahead;
-        if (s + 1 < steps) ahead = row_of(s + 1);
+        if (s + 1 < v.s1) ahead = row_of(s + 1);
         if (!mbar_wait_warp(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) {
           ok = false;
           break;
@@ -202,10 +231,8 @@ __global__ void __launch_bounds__(THREADS)
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_par = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += step) {
-      const Unit v = unit_of(u, table, g);
-      const int steps = (v.n + OT - 1) / OT;
-      for (int s = 0; s < steps; ++s) {
+    while (ok && v.next(line, g)) {
+      for (int s = v.s0; s < v.s1; ++s) {
         if (!mbar_wait_warp(saddr(&empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) {
           ok = false;
           break;
@@ -248,43 +275,48 @@ __global__ void __launch_bounds__(THREADS)
     int stage = 0, it = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += step, ++it) {
-      const Unit v = unit_of(u, table, g);
-      const int steps = (v.n + OT - 1) / OT, buf = it & (g.bufs - 1);
-      if (!mbar_wait_warp(saddr(&tempty[buf]), ((uint32_t)(it >> (g.bufs - 1)) & 1u) ^ 1u,
-                          abort_flag, g.status, limit))
-        break;
-      tc_fence_after();
-      const uint32_t acc = tmem + (uint32_t)(buf * 4 * g.n_mma);
-      for (int s = 0; s < steps; ++s) {
-        if (!mbar_wait_warp(saddr(&full[stage]), phase, abort_flag, g.status, limit)) {
+    while (ok && v.next(line, g)) {
+      int s = v.s0;
+      do {  // chains of at most CHAIN steps
+        const int c0 = s, c1 = min(v.s1, s + CHAIN), buf = it & (g.bufs - 1);
+        if (!mbar_wait_warp(saddr(&tempty[buf]), ((uint32_t)(it >> (g.bufs - 1)) & 1u) ^ 1u,
+                            abort_flag, g.status, limit)) {
           ok = false;
           break;
         }
-        fence_proxy_async_smem();  // the gathered rows (cp.async) -> MMA reads
         tc_fence_after();
-        if (elect_one()) {
-          const uint64_t so = (uint64_t)((stage * st_bytes) >> 4);
+        const uint32_t acc = tmem + (uint32_t)(buf * 4 * g.n_mma);
+        for (; s < c1; ++s) {
+          if (!mbar_wait_warp(saddr(&full[stage]), phase, abort_flag, g.status, limit)) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_smem();  // the gathered rows (cp.async) -> MMA reads
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t so = (uint64_t)((stage * st_bytes) >> 4);
 #pragma unroll
-          for (int q = 0; q < 3; ++q)
+            for (int q = 0; q < 3; ++q)
 #pragma unroll
-            for (int kk = 0; kk < OT / 16; ++kk)
+              for (int kk = 0; kk < OT / 16; ++kk)
 #pragma unroll
-              for (int m = 0; m < 2; ++m)
-                tc_mma<1>(acc + (uint32_t)(((q > 0 ? 2 : 0) + m) * g.n_mma),
-                          bd0 + so + (uint64_t)((m * 2 * CHUNK + kk * 2048) >> 4),
-                          pd0 + so + (uint64_t)((q * p_bytes + kk * 2048) >> 4), idesc,
-                          (s > 0 || q > 1 || kk > 0) ? 1u : 0u);
-          tc_commit<1>(saddr(&empty[stage]));
+                for (int m = 0; m < 2; ++m)
+                  tc_mma<1>(acc + (uint32_t)(((q > 0 ? 2 : 0) + m) * g.n_mma),
+                            bd0 + so + (uint64_t)((m * 2 * CHUNK + kk * 2048) >> 4),
+                            pd0 + so + (uint64_t)((q * p_bytes + kk * 2048) >> 4), idesc,
+                            (s > c0 || q > 1 || kk > 0) ? 1u : 0u);
+            tc_commit<1>(saddr(&empty[stage]));
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
+        if (ok && elect_one()) tc_commit<1>(saddr(&tfull[buf]));
         __syncwarp();
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      if (ok && elect_one()) tc_commit<1>(saddr(&tfull[buf]));
-      __syncwarp();
+        ++it;
+      } while (ok && s < v.s1);
     }
     if (elect_one()) tc_commit<1>(saddr(&done));
     __syncwarp();
@@ -296,46 +328,66 @@ __global__ void __launch_bounds__(THREADS)
   } else {
     // ------------------------------------------------------------ store
     const int q = warp & 3;  // TMEM lanes 32 q ...: columns of x or d_y
-    const size_t wide = (size_t)(g.D[0] + g.D[1]) * g.r;
     int it = 0;
-    for (int u = blockIdx.x; u < units; u += step, ++it) {
-      const Unit v = unit_of(u, table, g);
-      const int buf = it & (g.bufs - 1), D = g.D[v.p];
-      float* dst = v.slot < 0 ? g.out[v.p] + (size_t)v.l * D * g.r
-                              : g.part + (size_t)v.slot * wide + (v.p ? (size_t)g.D[0] * g.r : 0);
-      if (!mbar_wait_warp(saddr(&tfull[buf]), (uint32_t)(it >> (g.bufs - 1)) & 1u, abort_flag,
-                          g.status, limit))
-        break;
-      tc_fence_after();
-      const uint32_t acc = tmem + (uint32_t)(buf * 4 * g.n_mma) + ((uint32_t)(q * 32) << 16);
+    bool ok = true;
+    while (ok && v.next(line, g)) {
+      const int D = g.D[v.p], width = v.slot < 0 ? D : OC;  // of the destination
+      float* dst = v.slot < 0 ? g.out[v.p] + (size_t)v.l * D * g.r +
+                                    (v.p ? (size_t)v.c0 : (size_t)v.c0 * g.r)
+                              : g.part + (size_t)v.slot * OC * g.r;
+      int s = v.s0;
+      do {
+        const int buf = it & (g.bufs - 1);
+        const bool more = s > v.s0;  // another chain of the same unit: added to what is there
+        if (!mbar_wait_warp(saddr(&tfull[buf]), (uint32_t)(it >> (g.bufs - 1)) & 1u, abort_flag,
+                            g.status, limit)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)(buf * 4 * g.n_mma) + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
-      for (int m = 0; m < 2; ++m) {
-        const int c = v.c0 + m * 128 + q * 32 + lane;
+        for (int m = 0; m < 2; ++m) {
+          const int c = m * 128 + q * 32 + lane;
 #pragma unroll 2
-        for (int j0 = 0; j0 < g.r; j0 += 8) {
-          uint32_t f[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, f2[8];
-          if (v.n > 0) {  // else no rows: zeros
-            tmem_ld8(acc + (uint32_t)(m * g.n_mma + j0), f);
-            tmem_ld8(acc + (uint32_t)((2 + m) * g.n_mma + j0), f2);
-            tmem_ld_wait();
+          for (int j0 = 0; j0 < g.r; j0 += 8) {
+            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (v.n > 0) {  // else no rows: zeros
+              uint32_t f1[8], f2[8];
+              tmem_ld8(acc + (uint32_t)(m * g.n_mma + j0), f1);
+              tmem_ld8(acc + (uint32_t)((2 + m) * g.n_mma + j0), f2);
+              tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              f[j] = __float_as_uint(__uint_as_float(f[j]) + __uint_as_float(f2[j]));
-          }
-          if (c >= D) continue;
-          if (v.p == 0) {
-            uint4* o = reinterpret_cast<uint4*>(dst + (size_t)c * g.r + j0);
-            o[0] = make_uint4(f[0], f[1], f[2], f[3]);
-            o[1] = make_uint4(f[4], f[5], f[6], f[7]);
-          } else {
+              for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(f1[j]) + __uint_as_float(f2[j]);
+            }
+            if (v.c0 + c >= D) continue;
+            if (v.p == 0) {
+              float4* o = reinterpret_cast<float4*>(dst + (size_t)c * g.r + j0);
+              float4 u0 = make_float4(f[0], f[1], f[2], f[3]);
+              float4 u1 = make_float4(f[4], f[5], f[6], f[7]);
+              if (more) {
+                const float4 w0 = o[0], w1 = o[1];
+                u0.x += w0.x; u0.y += w0.y; u0.z += w0.z; u0.w += w0.w;
+                u1.x += w1.x; u1.y += w1.y; u1.z += w1.z; u1.w += w1.w;
+              }
+              o[0] = u0;
+              o[1] = u1;
+            } else {
+              float* o = dst + (size_t)j0 * width + c;
+              if (more)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dst[(size_t)(j0 + j) * D + c] = __uint_as_float(f[j]);
+                for (int j = 0; j < 8; ++j) f[j] += o[(size_t)j * width];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[(size_t)j * width] = f[j];
+            }
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(saddr(&tempty[buf]));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(saddr(&tempty[buf]));
+        s = min(v.s1, s + CHAIN);
+        ++it;
+      } while (s < v.s1);
     }
   }
   __syncwarp();  // lanes that waited alone are back
@@ -345,81 +397,71 @@ __global__ void __launch_bounds__(THREADS)
     tc_fence_after();
     tmem_dealloc<1>(tmem, tcols);
   }
+  if (g.early) pdl_wait();  // what follows this kernel finds the one before it complete, too
 }
 
-// dA and dB of the adapters with several chunks: their partial sums in chunk order. CTA (piece,
-// adapter): 4096 of the adapter's (D0 + D1) r values.
-constexpr int SUM_THREADS = 256, SUM_PIECE = 4 * 4 * SUM_THREADS;
+// The units that pieces end inside: their partial sums in the order of the pieces. CTA (share of
+// a unit, piece boundary); the first boundary inside a unit stands for it.
+constexpr int SUM_THREADS = 256, SUM_PIECE = 2 * 4 * SUM_THREADS;
 __global__ void __launch_bounds__(SUM_THREADS) adapter_outer_sum_kernel(const OuterArgs g) {
-  __shared__ int s_before[SUM_THREADS / 32];
+  __shared__ Line line;
   pdl_wait();  // the previous kernel in the stream has completed
   pdl_trigger();
-  const int tid = threadIdx.x, l = blockIdx.y;
-  auto chunks = [&](int a) {
-    const int n = (g.offsets[a + 1] - g.offsets[a] + g.chunk - 1) / g.chunk;
-    return n > 1 ? n : 0;
-  };
-  const int n = chunks(l);
-  if (n == 0) return;
-  int before = tid < l ? chunks(tid) : 0;  // L <= 256
-  before = __reduce_add_sync(0xffffffffu, before);
-  if ((tid & 31) == 0) s_before[tid >> 5] = before;
+  const int tid = threadIdx.x, c = (int)blockIdx.y + 1;
+  if (tid < 32) make_line(line, g);
   __syncthreads();
-  int base = 0;
+  const FewPieces pc = pieces_of(line, g);
+  if (c >= pc.n) return;
+  const int b = pc.begin(c), l = adapter_at(b, line, g.L);
+  const int steps = steps_of(l, g), w = steps + g.store, ct = (b - line.base[l]) / w;
+  const int u0 = line.base[l] + ct * w;
+  if (b == u0 || b - u0 >= steps || pc.begin(c - 1) > u0) return;
+  const int end = pc.of(u0 + steps - 1);  // the last piece with a part of the unit
+  const int p = ct >= g.tiles[0] ? 1 : 0, c0 = (ct - (p ? g.tiles[0] : 0)) * OC, D = g.D[p];
+  float* out = g.out[p] + (size_t)l * D * g.r + (p ? (size_t)c0 : (size_t)c0 * g.r);
+  const size_t size = (size_t)OC * g.r;
+  const float* p0 = g.part + (size_t)(2 * c - 1) * size;  // piece c - 1 ends here, c ... go on
+  float4 v[2];
+  int at[2];
 #pragma unroll
-  for (int i = 0; i < SUM_THREADS / 32; ++i) base += s_before[i];
-  const size_t na = (size_t)g.D[0] * g.r, wide = na + (size_t)g.D[1] * g.r;
-  const float* p0 = g.part + (size_t)base * wide;
-  float4 v[4];
-  size_t at[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    at[i] = (size_t)blockIdx.x * SUM_PIECE + (size_t)(i * SUM_THREADS + tid) * 4;
-    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < 2; ++i) {
+    at[i] = (int)blockIdx.x * SUM_PIECE + (i * SUM_THREADS + tid) * 4;
+    if (at[i] < (int)size) v[i] = *reinterpret_cast<const float4*>(p0 + at[i]);
   }
-#pragma unroll 2
-  for (int q = 0; q < n; ++q)
+#pragma unroll 4
+  for (int q = c; q <= end; ++q)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (at[i] < wide) {
-        const float4 u = *reinterpret_cast<const float4*>(p0 + (size_t)q * wide + at[i]);
+    for (int i = 0; i < 2; ++i)
+      if (at[i] < (int)size) {
+        const float4 u = *reinterpret_cast<const float4*>(g.part + (size_t)(2 * q) * size + at[i]);
         v[i].x += u.x; v[i].y += u.y; v[i].z += u.z; v[i].w += u.w;
       }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (at[i] < wide)  // D0 r is a multiple of four: a vector lies in one of the two
-      *reinterpret_cast<float4*>(at[i] < na
-                                     ? g.out[0] + (size_t)l * na + at[i]
-                                     : g.out[1] + (size_t)l * (wide - na) + (at[i] - na)) = v[i];
+  for (int i = 0; i < 2; ++i) {
+    if (at[i] >= (int)size) continue;
+    // [column][r] or [r][256 columns]; columns behind the last were not written
+    const int col = p ? at[i] % OC : at[i] / g.r;
+    if (c0 + col >= D) continue;
+    *reinterpret_cast<float4*>(p ? out + (size_t)(at[i] / OC) * D + col : out + at[i]) = v[i];
+  }
 }
 
 int tiles_of(int d) { return (d + OC - 1) / OC; }
 
-// Rows of a unit: enough units for four a SM, at least 512 rows each.
-int chunk_of(int T, int d_in, int d_out) {
-  long long c = (long long)T * (tiles_of(d_in) + tiles_of(d_out)) / (4 * 148);
-  c = (c + 63) / 64 * 64;
-  return (int)(c < 512 ? 512 : c);
-}
+// Pieces: two CTAs an SM, of 256 TMEM columns each (one for a rank above 64, which takes all 512).
+int ctas_of(int r) { return (r <= 64 ? 2 : 1) * sm_count(); }
 
 }  // namespace
 
-// Partial sums of adapters with more than one chunk: at most 2 T / chunk chunks.
-size_t adapter_outer_part_bytes(int T, int d_in, int d_out, int r) {
-  const size_t chunks = 2 * (size_t)(T / chunk_of(T, d_in, d_out));
-  return chunks * (size_t)(d_in + d_out) * r * 4;
+// Partial sums: two a piece.
+size_t adapter_outer_part_bytes(int T, int r) {
+  return T <= WHOLE_ROWS ? 0 : (size_t)2 * ctas_of(r) * OC * r * 4;
 }
 
-moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
-                                const void* d_y, const void* planes_d_low,
-                                const void* planes_low, const int32_t* offsets,
-                                const int32_t* rows, float* d_a, float* d_b, float* part,
-                                cudaStream_t st) {
+namespace {
+OuterArgs outer_args(int T, int d_in, int d_out, int r, int L, const int32_t* offsets,
+                     float* d_a, float* d_b, float* part) {
   OuterArgs a = {};
-  a.big[0] = (const bf16*)x;
-  a.big[1] = (const bf16*)d_y;
-  a.planes[0] = (const bf16*)planes_d_low;
-  a.planes[1] = (const bf16*)planes_low;
   a.out[0] = d_a;
   a.out[1] = d_b;
   a.D[0] = d_in;
@@ -427,12 +469,30 @@ moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const 
   a.tiles[0] = tiles_of(d_in);
   a.tiles[1] = tiles_of(d_out);
   a.offsets = offsets;
-  a.rows = rows;
   a.part = part;
   a.T = T;
   a.r = r;
   a.L = L;
-  a.chunk = chunk_of(T, d_in, d_out);
+  a.ctas = ctas_of(r);
+  a.cut = T > WHOLE_ROWS;
+  a.store = 1 + r / 32;
+  return a;
+}
+}  // namespace
+
+// early: the kernel launched last is the large product, which waited for all that is read here.
+moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
+                                const void* d_y, const void* planes_d_low,
+                                const void* planes_low, const int32_t* offsets,
+                                const int32_t* rows, float* d_a, float* d_b, float* part,
+                                bool early, cudaStream_t st) {
+  OuterArgs a = outer_args(T, d_in, d_out, r, L, offsets, d_a, d_b, part);
+  a.big[0] = (const bf16*)x;
+  a.big[1] = (const bf16*)d_y;
+  a.planes[0] = (const bf16*)planes_d_low;
+  a.planes[1] = (const bf16*)planes_low;
+  a.rows = rows;
+  a.early = early;
   a.n_mma = (r + 15) / 16 * 16;
   a.nc = (r + 63) / 64;
   a.bufs = a.n_mma <= 32 ? 2 : 1;
@@ -448,17 +508,20 @@ moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const 
   if (!make_map(&m0, planes_d_low, 3, pd, ps, pbox) || !make_map(&m1, planes_low, 3, pd, ps, pbox))
     return MOE_ERR_CUDA;
   launch_begin(K_ADAPTER_OUTER, st);
-  // two CTAs an SM, of 256 TMEM columns each (one for a rank above 64, which takes all 512)
-  const long long most = (long long)(T / a.chunk + L) * (a.tiles[0] + a.tiles[1]);
-  const int ctas = (a.nc == 1 ? 2 : 1) * sm_count();
-  launch_kernel(adapter_outer_kernel, dim3((unsigned)(most < ctas ? most : ctas)), dim3(THREADS),
-                (size_t)smem, st, 1, m0, m1, a);
-  const moe_status s = launch_end(K_ADAPTER_OUTER, st);
-  if (s != MOE_OK || T <= a.chunk) return s;
-  const size_t wide = (size_t)(d_in + d_out) * r;
+  launch_kernel(adapter_outer_kernel, dim3((unsigned)a.ctas), dim3(THREADS), (size_t)smem, st, 1,
+                m0, m1, a);
+  return launch_end(K_ADAPTER_OUTER, st);
+}
+
+// After launch_adapter_outer (and whatever may come between): the units that were cut.
+moe_status launch_adapter_outer_sum(int T, int d_in, int d_out, int r, int L,
+                                    const int32_t* offsets, float* d_a, float* d_b, float* part,
+                                    cudaStream_t st) {
+  const OuterArgs a = outer_args(T, d_in, d_out, r, L, offsets, d_a, d_b, part);
+  if (!a.cut) return MOE_OK;
   launch_begin(K_ADAPTER_OUTER_SUM, st);
   launch_kernel(adapter_outer_sum_kernel,
-                dim3((unsigned)((wide + SUM_PIECE - 1) / SUM_PIECE), (unsigned)L),
+                dim3((unsigned)((OC * r + SUM_PIECE - 1) / SUM_PIECE), (unsigned)(a.ctas - 1)),
                 dim3(SUM_THREADS), 0, st, 1, a);
   return launch_end(K_ADAPTER_OUTER_SUM, st);
 }
