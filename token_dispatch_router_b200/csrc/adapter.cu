@@ -30,8 +30,7 @@ moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapt
                                const void* in, const void* w, const AdapterTile* tiles,
                                const void* low, const void* m, void* out, float* part,
                                cudaStream_t st);
-moe_status launch_adapter_gemm_sum(int T, int k_dim, int n_out, void* out, float* part,
-                                   cudaStream_t st);
+AdapterTileSums adapter_gemm_sums(int T, int k_dim, int n_out, void* out, const float* part);
 size_t adapter_gemm_part_bytes(int T, int k_dim, int n_out);
 size_t adapter_outer_part_bytes(int T, int r);
 moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
@@ -39,9 +38,10 @@ moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const 
                                 const void* planes_low, const int32_t* offsets,
                                 const int32_t* rows, float* d_a, float* d_b, float* part,
                                 bool early, cudaStream_t st);
-moe_status launch_adapter_outer_sum(int T, int d_in, int d_out, int r, int L,
-                                    const int32_t* offsets, float* d_a, float* d_b, float* part,
-                                    cudaStream_t st);
+AdapterUnitSums adapter_outer_sums(int T, int d_in, int d_out, int r, float* d_a, float* d_b,
+                                   const float* part);
+moe_status launch_adapter_sum(const AdapterTileSums& a, const AdapterUnitSums& b,
+                              cudaStream_t st);
 
 namespace {
 
@@ -147,7 +147,8 @@ moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, con
                                (const AdapterTile*)(ws + L.tiles), ws + L.terms, b, y, part,
                                st)) != MOE_OK)
     return r;
-  return launch_adapter_gemm_sum(s.T, s.d_in, s.d_out, y, part, st);
+  return launch_adapter_sum(adapter_gemm_sums(s.T, s.d_in, s.d_out, y, part), AdapterUnitSums{},
+                            st);
 }
 
 moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, const void* x,
@@ -173,16 +174,14 @@ moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, 
                                (const AdapterTile*)(ws + L.tiles), ws + L.terms, a, d_x,
                                gemm_part, st)) != MOE_OK)
     return r;
-  // the outer products start as the large product's CTAs leave; both sums come behind them
+  // the outer products start as the large product's CTAs leave; what both leave is added last
   if ((r = launch_adapter_outer(s.T, s.d_in, s.d_out, s.rank, s.n_adapters, x, d_y,
                                 ws + L.planes_d, ws + L.planes_l, offsets, rows, d_a, d_b, part,
                                 d_x != nullptr, st)) != MOE_OK)
     return r;
-  if (d_x != nullptr && (r = launch_adapter_gemm_sum(s.T, s.d_out, s.d_in, d_x, gemm_part, st)) !=
-                            MOE_OK)
-    return r;
-  return launch_adapter_outer_sum(s.T, s.d_in, s.d_out, s.rank, s.n_adapters, offsets, d_a, d_b,
-                                  part, st);
+  return launch_adapter_sum(d_x != nullptr ? adapter_gemm_sums(s.T, s.d_out, s.d_in, d_x, gemm_part)
+                                           : AdapterTileSums{},
+                            adapter_outer_sums(s.T, s.d_in, s.d_out, s.rank, d_a, d_b, part), st);
 }
 
 }  // namespace moe

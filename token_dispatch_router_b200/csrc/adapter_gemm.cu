@@ -23,7 +23,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int BM = 128, PAIR_M = 256, BK = 64, BN = 256, STAGES = 6;
+constexpr int BM = 128, PAIR_M = kAdapterTileRows, BK = 64, BN = kAdapterTileCols, STAGES = 6;
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int B_CHUNK = BK * 64 * 2;
 constexpr int B_HALF = 2 * B_CHUNK;
@@ -32,7 +32,6 @@ constexpr int THREADS = 192;                   // producer, MMA, 4 epilogue warp
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int SMEM_TAIL = 512;
 constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SMEM_TAIL;
-constexpr int GROUP_M = 8;  // row tiles that share the W panels of a wave through L2
 
 struct AdapterGemmArgs {
   int T, n_out, kblocks, mt, nt, rank;
@@ -66,14 +65,6 @@ __device__ __forceinline__ Item item_of(int w, const AdapterGemmArgs& g) {
   const int v = w - g.whole, s = v % g.split;
   return Item{g.whole + v / g.split, s, s * g.kblocks / g.split, (s + 1) * g.kblocks / g.split,
               false, s == g.split - 1};
-}
-
-// Tile w: GROUP_M row tiles at a time, all column tiles of the group.
-__device__ __forceinline__ void tile_of(int w, int mt, int nt, int& m, int& n) {
-  const int per = GROUP_M * nt, grp = w / per, r = w % per;
-  const int gm = min(GROUP_M, mt - grp * GROUP_M);
-  m = grp * GROUP_M + r % gm;
-  n = r / gm;
 }
 
 template <bool BWD>
@@ -124,9 +115,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   // low and the table of tiles come from the kernel before this one; x, d_y, W and the adapters
   // are older (that kernel lets this one start only once all before it is complete). So only the
-  // adapter term waits for it (backward, 300 rows: 23.7 us with the wait here,
-  // 19.8 without). A CTA's shared
-  // memory leaves no room for one of that kernel, whose TMEM it could otherwise hold up.
+  // adapter term waits for it (backward, 300 rows: 23.7 us with the wait here, 19.8
+  // without). A CTA's shared memory leaves no room beside it for one of that kernel, whose TMEM it
+  // could otherwise hold up.
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
@@ -155,7 +146,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int w = pair; w < total && ok; w += npairs) {
         const Item it = item_of(w, g);
         int m, n;
-        tile_of(it.tile, g.mt, g.nt, m, n);
+        adapter_tile_of(it.tile, g.mt, g.nt, m, n);
         const int m0 = m * PAIR_M + (int)rank * BM, n0 = n * BN + (int)rank * 128;
         uint32_t fb, a;
         for (int kb = it.k0; kb < it.k1; ++kb) {
@@ -235,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int w = pair; w < total && ok; w += npairs, ++it) {
         const Item wi = item_of(w, g);
         int m, n;
-        tile_of(wi.tile, g.mt, g.nt, m, n);
+        adapter_tile_of(wi.tile, g.mt, g.nt, m, n);
         const int buf = it & 1;
         const uint32_t use = (uint32_t)(it >> 1);
         if (!mbar_wait<true>(saddr(&tempty[buf]), (use & 1u) ^ 1u, abort_flag, g.status, limit))
@@ -306,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int w = pair; w < total; w += npairs, ++it) {
       const Item wi = item_of(w, g);
       int m, n;
-      tile_of(wi.tile, g.mt, g.nt, m, n);
+      adapter_tile_of(wi.tile, g.mt, g.nt, m, n);
       const int buf = it & 1;
       const uint32_t use = (uint32_t)(it >> 1);
       if (first)
@@ -363,32 +354,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// The tiles behind the whole ones: their splits' partials in order, eight columns of a row a
-// thread. CTA (row and column group, tile).
-constexpr int SUM_THREADS = 256;
-__global__ void __launch_bounds__(SUM_THREADS) adapter_gemm_sum_kernel(const AdapterGemmArgs g) {
-  const int i = (int)blockIdx.x * SUM_THREADS + (int)threadIdx.x, tile = g.whole + (int)blockIdx.y;
-  const int lr = i % BM, c8 = i / BM % (BN / 8), half = i / BM / (BN / 8);
-  int m, n;
-  tile_of(tile, g.mt, g.nt, m, n);
-  const int r = m * PAIR_M + half * BM + lr, col = n * BN + c8 * 8;
-  pdl_wait();  // the previous kernel in the stream has completed
-  pdl_trigger();
-  if (r >= g.T || col >= g.n_out) return;
-  const float4* p0 = reinterpret_cast<const float4*>(g.part) +
-                     ((size_t)blockIdx.y * g.split * 2 + half) * (BN / 4) * BM +
-                     (size_t)c8 * 2 * BM + lr;
-  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int s = 0; s < g.split; ++s) {
-    const float4* pp = p0 + (size_t)s * 2 * (BN / 4) * BM;
-    const float4 u = __ldcg(pp), v = __ldcg(pp + BM);
-    f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
-    f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
-  }
-  *reinterpret_cast<uint4*>(g.out + (size_t)r * g.n_out + col) = pack16(f, bf16());
-}
-
 template <bool BWD>
 moe_status run(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& ml,
                const CUtensorMap& mm, const AdapterGemmArgs& a, cudaStream_t st) {
@@ -408,7 +373,7 @@ moe_status run(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& 
 
 // Tiles that do not fill the pairs of SMs once more are cut along the contraction, so that they
 // take that part of a tile's time: at most eight splits of at least four k-blocks, whose fp32
-// partials a second kernel adds in order. (2880 x 2880, 2049 rows: 108 tiles on 74 pairs took two
+// partials another kernel adds in order. (2880 x 2880, 2049 rows: 108 tiles on 74 pairs took two
 // rounds.) Returns the number of partials.
 int adapter_gemm_split(int T, int k_dim, int n_out, int* whole, int* split) {
   const int pairs = sm_count() > 1 ? sm_count() / 2 : 1;  // a host without a device counts one SM
@@ -434,8 +399,11 @@ size_t adapter_gemm_part_bytes(int T, int k_dim, int n_out) {
 
 // in [T, k_dim], w [d_in, d_out]; forward: k_dim = d_in, out [T, d_out], m = B; backward:
 // k_dim = d_out, out [T, d_in], m = A. low: [2][T][rank] bf16 terms.
-namespace {
-AdapterGemmArgs gemm_args(int T, int k_dim, int n_out, void* out, float* part) {
+moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
+                               const void* in, const void* w, const AdapterTile* tiles,
+                               const void* low, const void* m, void* out, float* part,
+                               cudaStream_t st) {
+  const int k_dim = bwd ? d_out : d_in, n_out = bwd ? d_in : d_out;
   AdapterGemmArgs a = {};
   a.T = T;
   a.n_out = n_out;
@@ -445,16 +413,6 @@ AdapterGemmArgs gemm_args(int T, int k_dim, int n_out, void* out, float* part) {
   adapter_gemm_split(T, k_dim, n_out, &a.whole, &a.split);
   a.part = part;
   a.out = (bf16*)out;
-  return a;
-}
-}  // namespace
-
-moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
-                               const void* in, const void* w, const AdapterTile* tiles,
-                               const void* low, const void* m, void* out, float* part,
-                               cudaStream_t st) {
-  const int k_dim = bwd ? d_out : d_in, n_out = bwd ? d_in : d_out;
-  AdapterGemmArgs a = gemm_args(T, k_dim, n_out, out, part);
   a.rank = rank;
   a.tiles = tiles;
   a.status = device_status_ptr();
@@ -475,16 +433,18 @@ moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapt
   return bwd ? run<true>(ma, mb, ml, mm, a, st) : run<false>(ma, mb, ml, mm, a, st);
 }
 
-// After launch_adapter_gemm (and whatever may come between): the tiles that were split.
-moe_status launch_adapter_gemm_sum(int T, int k_dim, int n_out, void* out, float* part,
-                                   cudaStream_t st) {
-  const AdapterGemmArgs a = gemm_args(T, k_dim, n_out, out, part);
-  if (a.split == 1) return MOE_OK;
-  launch_begin(K_ADAPTER_GEMM_SUM, st);
-  launch_kernel(adapter_gemm_sum_kernel,
-                dim3(PAIR_M * BN / 8 / SUM_THREADS, (unsigned)(a.mt * a.nt - a.whole)),
-                dim3(SUM_THREADS), 0, st, 1, a);
-  return launch_end(K_ADAPTER_GEMM_SUM, st);
+// What launch_adapter_gemm leaves to add.
+AdapterTileSums adapter_gemm_sums(int T, int k_dim, int n_out, void* out, const float* part) {
+  AdapterTileSums s = {};
+  s.T = T;
+  s.n_out = n_out;
+  s.mt = (T + PAIR_M - 1) / PAIR_M;
+  s.nt = (n_out + BN - 1) / BN;
+  adapter_gemm_split(T, k_dim, n_out, &s.whole, &s.split);
+  s.others = s.mt * s.nt - s.whole;
+  s.part = part;
+  s.out = (bf16*)out;
+  return s;
 }
 
 }  // namespace moe

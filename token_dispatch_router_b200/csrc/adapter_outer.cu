@@ -34,7 +34,7 @@ namespace {
 using namespace ptx;
 
 constexpr int LOADERS = 128, THREADS = 320;  // four gather warps, MMA, TMA, four store warps
-constexpr int OC = 256;                      // columns of a unit
+constexpr int OC = kAdapterUnitCols;         // columns of a unit
 constexpr int OT = 32;                       // rows per stage
 constexpr int STAGES = 3;
 constexpr int CHUNK = OT * 128;              // OT rows x 64 columns
@@ -51,6 +51,7 @@ struct OuterArgs {
   const int32_t* offsets;
   const int32_t* rows;
   float* part;        // [2 CTAs][256 r]: the units that a piece begins and ends inside
+  AdapterCut* cuts;    // [CTAs]
   int T, r, L;
   int ctas, cut;      // pieces at most; whether a piece may end inside a unit
   int store;          // positions of a unit's stores
@@ -133,6 +134,19 @@ struct Walk {
   }
 };
 
+// Whether this CTA's piece is the first that begins inside a unit.
+__device__ __forceinline__ AdapterCut cut_of(const Line& t, const OuterArgs& g) {
+  const FewPieces pc = pieces_of(t, g);
+  const int c = blockIdx.x;
+  if (c == 0 || c >= pc.n) return AdapterCut{-1, 0, 0, 0};
+  const int b = pc.begin(c), l = adapter_at(b, t, g.L);
+  const int steps = steps_of(l, g), w = steps + g.store, ct = (b - t.base[l]) / w;
+  const int u0 = t.base[l] + ct * w;
+  if (b == u0 || b - u0 >= steps || pc.begin(c - 1) > u0) return AdapterCut{-1, 0, 0, 0};
+  const int p = ct >= g.tiles[0] ? 1 : 0;
+  return AdapterCut{l, p, (ct - (p ? g.tiles[0] : 0)) * OC, pc.of(u0 + steps - 1)};
+}
+
 __global__ void __launch_bounds__(THREADS)
     adapter_outer_kernel(const __grid_constant__ CUtensorMap tmP0,
                          const __grid_constant__ CUtensorMap tmP1, const OuterArgs g) {
@@ -175,6 +189,7 @@ __global__ void __launch_bounds__(THREADS)
   const uint32_t tmem = s_tmem;
   const uint64_t limit = g.limit_ns;
   Walk v(line, g);
+  if (g.cut && tid == 0) g.cuts[blockIdx.x] = cut_of(line, g);
 
   if (warp < 4) {
     // ------------------------------------------------------------ gather
@@ -400,52 +415,6 @@ __global__ void __launch_bounds__(THREADS)
   if (g.early) pdl_wait();  // what follows this kernel finds the one before it complete, too
 }
 
-// The units that pieces end inside: their partial sums in the order of the pieces. CTA (share of
-// a unit, piece boundary); the first boundary inside a unit stands for it.
-constexpr int SUM_THREADS = 256, SUM_PIECE = 2 * 4 * SUM_THREADS;
-__global__ void __launch_bounds__(SUM_THREADS) adapter_outer_sum_kernel(const OuterArgs g) {
-  __shared__ Line line;
-  pdl_wait();  // the previous kernel in the stream has completed
-  pdl_trigger();
-  const int tid = threadIdx.x, c = (int)blockIdx.y + 1;
-  if (tid < 32) make_line(line, g);
-  __syncthreads();
-  const FewPieces pc = pieces_of(line, g);
-  if (c >= pc.n) return;
-  const int b = pc.begin(c), l = adapter_at(b, line, g.L);
-  const int steps = steps_of(l, g), w = steps + g.store, ct = (b - line.base[l]) / w;
-  const int u0 = line.base[l] + ct * w;
-  if (b == u0 || b - u0 >= steps || pc.begin(c - 1) > u0) return;
-  const int end = pc.of(u0 + steps - 1);  // the last piece with a part of the unit
-  const int p = ct >= g.tiles[0] ? 1 : 0, c0 = (ct - (p ? g.tiles[0] : 0)) * OC, D = g.D[p];
-  float* out = g.out[p] + (size_t)l * D * g.r + (p ? (size_t)c0 : (size_t)c0 * g.r);
-  const size_t size = (size_t)OC * g.r;
-  const float* p0 = g.part + (size_t)(2 * c - 1) * size;  // piece c - 1 ends here, c ... go on
-  float4 v[2];
-  int at[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    at[i] = (int)blockIdx.x * SUM_PIECE + (i * SUM_THREADS + tid) * 4;
-    if (at[i] < (int)size) v[i] = *reinterpret_cast<const float4*>(p0 + at[i]);
-  }
-#pragma unroll 4
-  for (int q = c; q <= end; ++q)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (at[i] < (int)size) {
-        const float4 u = *reinterpret_cast<const float4*>(g.part + (size_t)(2 * q) * size + at[i]);
-        v[i].x += u.x; v[i].y += u.y; v[i].z += u.z; v[i].w += u.w;
-      }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (at[i] >= (int)size) continue;
-    // [column][r] or [r][256 columns]; columns behind the last were not written
-    const int col = p ? at[i] % OC : at[i] / g.r;
-    if (c0 + col >= D) continue;
-    *reinterpret_cast<float4*>(p ? out + (size_t)(at[i] / OC) * D + col : out + at[i]) = v[i];
-  }
-}
-
 int tiles_of(int d) { return (d + OC - 1) / OC; }
 
 // Pieces: two CTAs an SM, of 256 TMEM columns each (one for a rank above 64, which takes all 512).
@@ -453,14 +422,17 @@ int ctas_of(int r) { return (r <= 64 ? 2 : 1) * sm_count(); }
 
 }  // namespace
 
-// Partial sums: two a piece.
+// Partial sums, two a piece, and the table of cuts.
 size_t adapter_outer_part_bytes(int T, int r) {
-  return T <= WHOLE_ROWS ? 0 : (size_t)2 * ctas_of(r) * OC * r * 4;
+  return T <= WHOLE_ROWS ? 0 : (size_t)ctas_of(r) * (2 * OC * r * 4 + sizeof(AdapterCut));
 }
 
-namespace {
-OuterArgs outer_args(int T, int d_in, int d_out, int r, int L, const int32_t* offsets,
-                     float* d_a, float* d_b, float* part) {
+// early: the kernel launched last is the large product, which waited for all that is read here.
+moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
+                                const void* d_y, const void* planes_d_low,
+                                const void* planes_low, const int32_t* offsets,
+                                const int32_t* rows, float* d_a, float* d_b, float* part,
+                                bool early, cudaStream_t st) {
   OuterArgs a = {};
   a.out[0] = d_a;
   a.out[1] = d_b;
@@ -470,23 +442,13 @@ OuterArgs outer_args(int T, int d_in, int d_out, int r, int L, const int32_t* of
   a.tiles[1] = tiles_of(d_out);
   a.offsets = offsets;
   a.part = part;
+  a.cuts = (AdapterCut*)(part + (size_t)2 * ctas_of(r) * OC * r);
   a.T = T;
   a.r = r;
   a.L = L;
   a.ctas = ctas_of(r);
   a.cut = T > WHOLE_ROWS;
   a.store = 1 + r / 32;
-  return a;
-}
-}  // namespace
-
-// early: the kernel launched last is the large product, which waited for all that is read here.
-moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const void* x,
-                                const void* d_y, const void* planes_d_low,
-                                const void* planes_low, const int32_t* offsets,
-                                const int32_t* rows, float* d_a, float* d_b, float* part,
-                                bool early, cudaStream_t st) {
-  OuterArgs a = outer_args(T, d_in, d_out, r, L, offsets, d_a, d_b, part);
   a.big[0] = (const bf16*)x;
   a.big[1] = (const bf16*)d_y;
   a.planes[0] = (const bf16*)planes_d_low;
@@ -513,17 +475,19 @@ moe_status launch_adapter_outer(int T, int d_in, int d_out, int r, int L, const 
   return launch_end(K_ADAPTER_OUTER, st);
 }
 
-// After launch_adapter_outer (and whatever may come between): the units that were cut.
-moe_status launch_adapter_outer_sum(int T, int d_in, int d_out, int r, int L,
-                                    const int32_t* offsets, float* d_a, float* d_b, float* part,
-                                    cudaStream_t st) {
-  const OuterArgs a = outer_args(T, d_in, d_out, r, L, offsets, d_a, d_b, part);
-  if (!a.cut) return MOE_OK;
-  launch_begin(K_ADAPTER_OUTER_SUM, st);
-  launch_kernel(adapter_outer_sum_kernel,
-                dim3((unsigned)((OC * r + SUM_PIECE - 1) / SUM_PIECE), (unsigned)(a.ctas - 1)),
-                dim3(SUM_THREADS), 0, st, 1, a);
-  return launch_end(K_ADAPTER_OUTER_SUM, st);
+// What launch_adapter_outer leaves to add.
+AdapterUnitSums adapter_outer_sums(int T, int d_in, int d_out, int r, float* d_a, float* d_b,
+                                   const float* part) {
+  AdapterUnitSums s = {};
+  s.D[0] = d_in;
+  s.D[1] = d_out;
+  s.r = r;
+  s.pieces = T > WHOLE_ROWS ? ctas_of(r) : 0;
+  s.part = part;
+  s.cuts = (const AdapterCut*)(part + (size_t)2 * ctas_of(r) * OC * r);
+  s.out[0] = d_a;
+  s.out[1] = d_b;
+  return s;
 }
 
 }  // namespace moe

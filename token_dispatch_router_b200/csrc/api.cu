@@ -144,8 +144,8 @@ const char* kKernelNames[K_COUNT] = {
     "permute_cluster", "tile_round", "bwd_act", "bwd_dw", "bwd_dx",
     "router_dlogits", "router_dwr", "router_dx", "omni_logits", "omni_topk", "omni_count",
     "omni_scan", "omni_scatter", "omni_sort", "omni_act", "omni_out", "few_route", "few_up",
-    "few_down", "few_sum", "adapter_few",  "adapter_low_few", "adapter_low", "adapter_gemm", "adapter_gemm_sum", "adapter_outer",
-    "adapter_outer_sum"};
+    "few_down",     "few_sum",       "adapter_few",    "adapter_low_few", "adapter_low", "adapter_gemm",
+    "adapter_outer", "adapter_sum"};
 
 struct ProfRec {
   int kid;

@@ -45,9 +45,8 @@ enum KernelId {
   K_ADAPTER_LOW_FEW,
   K_ADAPTER_LOW,
   K_ADAPTER_GEMM,
-  K_ADAPTER_GEMM_SUM,
   K_ADAPTER_OUTER,
-  K_ADAPTER_OUTER_SUM,
+  K_ADAPTER_SUM,
   K_COUNT
 };
 
