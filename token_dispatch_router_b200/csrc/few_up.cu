@@ -19,6 +19,8 @@
 // the MMAs (two accumulators, double-buffered), warps 4-7 read them (lane = weight column, column
 // = token). Every wait is bounded; on expiry
 // the status word records MOE_ERR_TIMEOUT and the CTA ends after its copies and MMAs in flight.
+#include <type_traits>
+
 #include "few.cuh"
 #include "few_args.cuh"
 #include "ffn_args.cuh"
@@ -291,27 +293,45 @@ __global__ void __launch_bounds__(THREADS, 1)
         epi_bar();
         if (t.last) {
           __threadfence();
-          // eight tokens at a time, so that their loads are in flight together
-          for (int j0 = 0; j0 < n_tok; j0 += 8) {
-            float gf[8], uf[8];
+          // 16 partials of a column at a time, so that their loads are in flight together: of
+          // eight tokens, or of the tile's pieces where there are few tokens
+          auto join = [&](auto tokens, auto pieces) {
+            constexpr int NT = decltype(tokens)::value, NP = decltype(pieces)::value;
+            for (int j0 = 0; j0 < n_tok; j0 += NT) {
+              float gf[NT], uf[NT];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) gf[i] = uf[i] = 0.f;
-            for (int p = p0; p <= p1; ++p) {
-              const int s = 2 * p + (tile0 >= cut.begin(p) ? 1 : 0);
-              const float* pp = g.part + ((size_t)s * g.T + j0) * 256 + cl;
+              for (int i = 0; i < NT; ++i) gf[i] = uf[i] = 0.f;
+              for (int p = p0; p <= p1; p += NP) {
+                float gv[NP][NT], uv[NP][NT];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (j0 + i < n_tok) {
-                  gf[i] += __ldcg(pp + i * 256);
-                  uf[i] += __ldcg(pp + i * 256 + 128);
+                for (int z = 0; z < NP; ++z) {
+                  const int s = 2 * (p + z) + (tile0 >= cut.begin(p + z) ? 1 : 0);
+                  const float* pp = g.part + ((size_t)s * g.T + j0) * 256 + cl;
+#pragma unroll
+                  for (int i = 0; i < NT; ++i) {
+                    const bool on = p + z <= p1 && j0 + i < n_tok;
+                    gv[z][i] = on ? __ldcg(pp + i * 256) : 0.f;
+                    uv[z][i] = on ? __ldcg(pp + i * 256 + 128) : 0.f;
+                  }
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (j0 + i < n_tok && col_ok)
-                act[(size_t)t.tok[j0 + i] * g.n] =
-                    __float2bfloat16(t.w[j0 + i] * silu_mul(gf[i], uf[i]));
-          }
+                for (int z = 0; z < NP; ++z)
+#pragma unroll
+                  for (int i = 0; i < NT; ++i) {
+                    gf[i] += gv[z][i];
+                    uf[i] += uv[z][i];
+                  }
+              }
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+                if (j0 + i < n_tok && col_ok)
+                  act[(size_t)t.tok[j0 + i] * g.n] =
+                      __float2bfloat16(t.w[j0 + i] * silu_mul(gf[i], uf[i]));
+            }
+          };
+          using std::integral_constant;
+          if (n_tok <= 2) join(integral_constant<int, 2>{}, integral_constant<int, 8>{});
+          else join(integral_constant<int, 8>{}, integral_constant<int, 2>{});
         }
       }
       b = stop;
