@@ -305,9 +305,10 @@ moe_status moe_forward_workspace_layout(const moe_shape* shape, moe_workspace_la
 
 /* ----------------------------------------------------------------------------
  * moe_decode - the whole layer for a few tokens (a serving step: one new token for each of
- * up to MOE_DECODE_MAX_TOKENS requests), in two kernels: the router, then both expert
- * products and the combine in one persistent kernel bound by reading each taken expert's
- * weights once. The pages have no counterpart (a deployment variant of moe_forward).
+ * up to MOE_DECODE_MAX_TOKENS requests), in four kernels: the router, the first expert
+ * product with its activation, the second one added up over the experts, and the sum of its
+ * partial tiles; bound by reading each taken expert's weights once. The pages have no
+ * counterpart (a deployment variant of moe_forward).
  * Computes what moe_forward computes, with the expert outputs kept in fp32 until the
  * combine (moe_forward rounds them to bf16 between its kernels):
  *   out[t] = sum_k w[t,k] (silu(x_t W_gate[e]) * (x_t W_up[e])) W_down[e],  e = id[t,k].
@@ -316,8 +317,9 @@ moe_status moe_forward_workspace_layout(const moe_shape* shape, moe_workspace_la
  * Results repeat bit for bit. ffn_variant and route_topk do not apply.
  * bf16 only; T <= MOE_DECODE_MAX_TOKENS; no tile_round: else MOE_ERR_UNSUPPORTED.
  * x, w_r, w_gate, w_up, w_down and out 16-byte aligned, workspace 256-byte aligned and
- * >= moe_decode_workspace_size(shape); nothing in it has to be set before a call or kept
- * after it. Calls that may run at the same time need a workspace each.
+ * >= moe_decode_workspace_size(shape) as given on the device that runs the call; nothing in it
+ * has to be set before a call or kept after it. Calls that may run at the same time need a
+ * workspace each. out may not overlap an input.
  */
 #define MOE_DECODE_MAX_TOKENS 128
 size_t moe_decode_workspace_size(const moe_shape* shape);
@@ -354,9 +356,10 @@ moe_status moe_decode(const moe_shape* shape, const void* x, const void* w_r, co
  * d_in and d_out multiples of 64, rank a multiple of 8, else MOE_ERR_INVALID_ARG; bf16 only,
  * rank <= 128, n_adapters <= 256, T <= 2^24, else MOE_ERR_UNSUPPORTED. Adapters of several
  * ranks: the largest one, the others padded with zeros. Every pointer except ids and scale
- * 16-byte aligned; workspace 256-byte aligned, >= moe_adapter_workspace_size(shape), nothing
- * in it has to be set before a call or kept after it. Calls that may run at the same time need
- * a workspace each. T = 0: forward does nothing, backward zeroes d_a and d_b.
+ * 16-byte aligned; workspace 256-byte aligned, >= moe_adapter_workspace_size(shape) as given on
+ * the device that runs the call, nothing in it has to be set before a call or kept after it.
+ * Calls that may run at the same time need a workspace each. Outputs may not overlap inputs.
+ * T = 0: forward does nothing, backward zeroes d_a and d_b.
  */
 typedef struct {
   int32_t T, d_in, d_out, n_adapters, rank;

@@ -119,8 +119,9 @@ __global__ void __launch_bounds__(THREADS)
   const uint32_t sb = saddr(base);
   const int st_bytes = X_BYTES + g.nc * M_CHUNK;
   volatile int* abort_flag = &s_abort;
-  // MMAs into one accumulator follow each other about 190 cycles apart however small they are:
-  // the k steps go round four accumulators (two of a rank above 64)
+  // The tensor core cuts what it adds to an accumulator off rather than rounding it: the k steps
+  // go round four accumulators (two of a rank above 64), which are added in fp32, so that the
+  // fp32 result stays near that of a rounded sum.
   const int accs = g.nc == 1 ? 4 : 2;
   uint32_t tcols = 32;
   while ((int)tcols < accs * g.n_mma) tcols *= 2;

@@ -70,7 +70,9 @@ __device__ __forceinline__ uint32_t lanemask_lt() {
 // Programmatic dependent launch. Every kernel of the library is launched with programmatic
 // stream serialisation, so the GPU may schedule it while the kernel before it in the stream
 // is still running. pdl_wait() returns once that kernel has completed and its writes are
-// visible: every kernel calls it before its first global-memory access (read or write).
+// visible: a kernel calls it before its first global-memory access (read or write). Some read
+// before it what is older than the kernel before them, which is sound where that kernel triggers
+// only after its own wait: all before it is complete by then (each says so where it does).
 // pdl_trigger() allows the next kernel to be scheduled once every CTA of this one has called
 // it (or exited); it does not make this kernel's writes visible early.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

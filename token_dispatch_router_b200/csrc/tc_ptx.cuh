@@ -13,9 +13,8 @@ __device__ __forceinline__ uint32_t saddr(const void* p) {
 }
 
 // One lane of a converged warp. Instructions that take uniform registers (tcgen05.mma, commit,
-// TMA) are issued under it from warp-uniform loops: from a branch on the lane index the compiler
-// has to move every operand out of a divergent thread first, which costs more than the issue
-// (a tcgen05.mma of 128 x 64 x 16: about 190 cycles against 60).
+// TMA) are issued under it from warp-uniform loops: from a branch on the lane index every operand
+// has to be moved out of a divergent thread first.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t p = 0;
   asm volatile(
