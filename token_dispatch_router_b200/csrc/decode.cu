@@ -71,6 +71,7 @@ moe_status launch_decode(const moe_shape& s, const void* x, const void* w_r, con
   dn.n = s.n;
   dn.d = s.d;
   dn.act = u.act;
+  dn.rows = L.active * s.T;
   dn.part = u.part;
   dn.ids = ids;
   dn.out = (bf16*)out;

@@ -9,7 +9,7 @@ struct FewUpArgs {
   int T, K, E, n, cap;
   const int32_t* ids;   // [T, K]
   const float* topk_w;  // [T, K]
-  bf16* act;            // [active experts][T][n]
+  bf16* act;            // [active experts][T][n]: row j is the expert's j-th token
   float* part;          // [2 pieces][T][256]
   uint32_t* arrived;    // [pieces], zero when the kernel starts
   // set by launch_few_up
@@ -21,7 +21,8 @@ struct FewUpArgs {
 struct FewDownArgs {
   int T, K, E, cap, n, d;
   const int32_t* ids;  // [T, K]
-  const bf16* act;     // [active experts][T][n]
+  const bf16* act;     // [active experts][T][n]: row j is the expert's j-th token
+  int rows;            // its rows: active experts (at most) times T
   bf16* out;           // [T, d]
   float* part;         // [2 pieces][T][128]: partials of cut tiles
   // set by the launcher

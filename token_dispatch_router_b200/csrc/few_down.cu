@@ -17,8 +17,8 @@
 // The weights do not depend on the kernel before this one: a CTA fills its ring with them before
 // it waits for that kernel (its launch follows that kernel's own wait, so everything older, the
 // ids among it, is complete).
-// Roles (256 threads): warp 0 copies weights by TMA, warps 1 and 3 the expert's rows of act by
-// cp.async, warp 2 issues the MMAs (two accumulators, so that one is added while the next is
+// Roles (256 threads): warp 0 copies weights, warp 1 the expert's rows of act, eight a copy (two
+// warps with cp.async: 30 us of 515 at 128 tokens, width 4096, 8 experts of 14336), warp 2 issues the MMAs (two accumulators, so that one is added while the next is
 // made), warps 4-7 add and store. A finished wait costs a warp about 200 cycles and a copy or an
 // MMA 60 to issue, so a stage is 128 k of 128 columns, 32 KB brought by one copy and taken by
 // eight MMAs.
@@ -38,7 +38,7 @@ using namespace ptx;
 constexpr int THREADS = 256;
 constexpr int BN = 128, BK = 128, PIECES = BK / 64;
 constexpr int W_BYTES = BN * BK * 2;
-constexpr int GATHER = 64;     // threads that copy rows
+constexpr int X_ROWS = 8;      // rows of act a copy
 constexpr int MAX_STAGES = 6;
 constexpr int MIN_BLOCKS = 2;  // stages of a piece, at least
 constexpr int SMEM_LIMIT = 227 * 1024;
@@ -66,7 +66,8 @@ __device__ __forceinline__ void tmem_st_wait() {
 }
 
 __global__ void __launch_bounds__(THREADS, 1)
-    few_down_kernel(const __grid_constant__ CUtensorMap tmW, const FewDownArgs g) {
+    few_down_kernel(const __grid_constant__ CUtensorMap tmW,
+                    const __grid_constant__ CUtensorMap tmX, const FewDownArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   Tail& t = *reinterpret_cast<Tail*>(base + g.ring_bytes);  // behind rows and weights
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* abort_flag = &t.abort;
   if (tid == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
-      mbar_init(saddr(&t.full[s]), 1 + GATHER);  // weights and rows
+      mbar_init(saddr(&t.full[s]), 2);  // weights and rows
       mbar_init(saddr(&t.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -86,7 +87,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init_fence();
   }
   if (warp == 2) tmem_alloc<1>(saddr(&t.tmem), TMEM_COLS);
-  if (tid == 96) prefetch_map(&tmW);
+  if (tid == 96) {
+    prefetch_map(&tmW);
+    prefetch_map(&tmX);
+  }
   few_clear_masks(t.m, g.E, THREADS);
   // ids: written by the kernel before the previous one, which is complete
   few_build_masks(t.m, g.ids, g.T, g.K, g.E, g.cap, THREADS);
@@ -147,15 +151,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       while (globaltimer_ns() - t0 < 1000000) {
       }
     }
-  } else if (warp == 1 || warp == 3) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------ rows of act
-    // a thread copies one 16-byte piece of a row of the stage, for every fourth of the tokens
-    constexpr int ROW_PIECES = BK / 8;
-    const int gt = lane + (warp == 3 ? 32 : 0), piece = gt % ROW_PIECES;
-    int a = at0 / g.kb, k = at0 % g.kb, e = 0, n_tok = 0;
+    // a lane copies 64 k of eight of the expert's tokens (what lies behind the last one fills
+    // columns that nobody reads; k behind n are zeros)
+    int a = at0 / g.kb, k = at0 % g.kb, groups = 0;
     auto enter = [&]() {
-      e = t.m.act[a];
-      n_tok = few_count(t.m.mask[e]);
+      groups = (few_count(t.m.mask[t.m.act[a]]) + X_ROWS - 1) / X_ROWS;
     };
     if (work) enter();
     pdl_wait();  // act is complete
@@ -163,15 +165,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t phase = 0;
     for (int b = b0; b < b1; ++b) {
       if (!mbar_wait_warp(saddr(&t.empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
-      const uint32_t x = ring + (uint32_t)stage * stage_bytes + W_BYTES +
-                         (uint32_t)(piece >> 3) * x_most;
-      const int col = k * BK + piece * 8;
-      const bf16* src = g.act + (size_t)a * g.T * g.n + (col < g.n ? col : 0);
-      const unsigned char* tok = t.tok + t.first[e];
-      for (int j = gt / ROW_PIECES; j < n_tok; j += GATHER / ROW_PIECES)
-        cp_async16_if(x + (uint32_t)(j * 128 + (((piece & 7) ^ (j & 7)) << 4)),
-                      src + (size_t)tok[j] * g.n, col < g.n);
-      cp_async_arrive_noinc(saddr(&t.full[stage]));
+      const uint32_t fb = saddr(&t.full[stage]);
+      if (lane == 0) mbar_expect_tx(fb, (uint32_t)(PIECES * groups * X_ROWS * 128));
+      __syncwarp();
+      const int piece = lane >= groups ? 1 : 0, grp = lane - piece * groups;
+      if (lane < PIECES * groups)
+        tma_load_2d(ring + (uint32_t)stage * stage_bytes + W_BYTES + (uint32_t)piece * x_most +
+                        (uint32_t)(grp * X_ROWS * 128),
+                    &tmX, k * BK + piece * 64, a * g.T + grp * X_ROWS, fb);
+      __syncwarp();
       if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
@@ -182,7 +184,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         enter();
       }
     }
-    cp_async_wait_all();
+    if (lane == 0 && *abort_flag) {  // as above
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000) {
+      }
+    }
   } else if (warp == 2) {
     // ------------------------------------------------------------ MMA issuer
     // D fp32, A and B bf16, A MN-major (bit 15), B K-major, M = 128, N = the expert's tokens
@@ -206,7 +212,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = false;
           break;
         }
-        fence_proxy_async_smem();  // the rows (cp.async) -> MMA reads
         tc_fence_after();
         if (elect_one()) {
           const uint64_t so = (uint64_t)(((uint32_t)stage * stage_bytes) >> 4);
@@ -235,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       while (!mbar_try(saddr(&t.done), 0) && globaltimer_ns() - t0 < limit) {
       }
     }
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, cl = q * 32 + lane;  // TMEM lane = output column of the tile
     const uint32_t tile_at = tmem + ((uint32_t)(q * 32) << 16);
@@ -357,15 +362,19 @@ moe_status launch_few_down(FewDownArgs a, const void* w_down, cudaStream_t st) {
   a.ring_bytes = (SMEM_LIMIT - fixed) / 1024 * 1024;
   a.status = device_status_ptr();
   a.limit_ns = kWaitLimitNs;
-  CUtensorMap mw;
-  if (!make_piece_map(&mw, w_down, a.n, a.d, a.E, BK, BN / 64)) return MOE_ERR_CUDA;
+  CUtensorMap mw, mx;
+  const uint64_t xd[2] = {(uint64_t)a.n, (uint64_t)a.rows}, xs[1] = {(uint64_t)a.n * 2};
+  const uint32_t xbox[2] = {64, X_ROWS};
+  if (!make_piece_map(&mw, w_down, a.n, a.d, a.E, BK, BN / 64) ||
+      !make_map(&mx, a.act, 2, xd, xs, xbox, false))
+    return MOE_ERR_CUDA;
   if (cudaFuncSetAttribute(few_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            SMEM_LIMIT) != cudaSuccess)
     return MOE_ERR_CUDA;
   const int ctas = sm_count();
   launch_begin(K_FEW_DOWN, st);
   launch_kernel(few_down_kernel, dim3((unsigned)ctas), dim3(THREADS),
-                (size_t)(fixed + a.ring_bytes), st, 1, mw, a);
+                (size_t)(fixed + a.ring_bytes), st, 1, mw, mx, a);
   const moe_status r = launch_end(K_FEW_DOWN, st);
   if (r != MOE_OK) return r;
   launch_begin(K_FEW_SUM, st);

@@ -1,6 +1,6 @@
 // First expert product of the few-token layer: for each expert e that keeps a token,
-//   act[a, t] = w[t, e] silu(x_t W_gate[e]) * (x_t W_up[e])      (a: e's place among them)
-// for its tokens t, at most 128 of them. w is the routing weight: the second product then only
+//   act[a, j] = w[t, e] silu(x_t W_gate[e]) * (x_t W_up[e])      (a: e's place among them)
+// for its tokens t (t its j-th one), at most 128 of them. w is the routing weight: the second product then only
 // adds up.
 //
 // Bound by reading W_gate and W_up of those experts. They are the MMA's A operand, 128 columns
@@ -45,8 +45,7 @@ struct Tail {
   uint32_t tmem;
   int abort, epi_ok, last;
   FewMasks m;
-  float w[kFewMaxTokens];         // the unit's expert: its tokens' routing weights
-  unsigned char tok[kFewMaxTokens];  // and the tokens, ascending
+  float w[kFewMaxTokens];  // the tile's expert: the routing weights of its tokens, ascending
 };
 
 // The j-th token of a mask (j below its count).
@@ -233,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool whole = b == tile0 && stop == tile1;
       const int a = tile / g.nt, e = t.m.act[a], ct = tile % g.nt;
       const int buf = it & 1;
-      if (e != last_e) {  // this expert's tokens and their weights
+      if (e != last_e) {  // the weights of this expert's tokens
         last_e = e;
         epi_bar();  // everyone is done with those of the expert before
         const unsigned(&m)[4] = t.m.mask[e];
@@ -242,7 +241,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             j += __popc(i < (et >> 5) ? m[i] : i == (et >> 5) ? m[i] & ((1u << (et & 31)) - 1u) : 0u);
-          t.tok[j] = (unsigned char)et;
           for (int k = 0; k < g.K; ++k)
             if (g.ids[et * g.K + k] == e) t.w[j] = g.topk_w[et * g.K + k];
         }
@@ -275,7 +273,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (j >= n_tok) continue;
           const float gf = __uint_as_float(gv[i]), uf = __uint_as_float(uv[i]);
           if (whole) {
-            if (col_ok) act[(size_t)t.tok[j] * g.n] = __float2bfloat16(t.w[j] * silu_mul(gf, uf));
+            if (col_ok) act[(size_t)j * g.n] = __float2bfloat16(t.w[j] * silu_mul(gf, uf));
           } else {
             part[(size_t)j * 256] = gf;
             part[(size_t)j * 256 + 128] = uf;
@@ -325,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int i = 0; i < NT; ++i)
                 if (j0 + i < n_tok && col_ok)
-                  act[(size_t)t.tok[j0 + i] * g.n] =
+                  act[(size_t)(j0 + i) * g.n] =
                       __float2bfloat16(t.w[j0 + i] * silu_mul(gf[i], uf[i]));
             }
           };
