@@ -12,7 +12,7 @@
 // with the MMA's lane mask (disable-output-lane) keeping it out of the other rows. Rows of one
 // tile may so belong to any adapters in any order, nothing is multiplied by zero (an infinity
 // or NaN in one adapter stays in its own rows), and the epilogue only stores. low is fp32: it
-// enters as two bf16 terms (error 2^-17), far inside the rounding of the output. The adapters of
+// enters as two bf16 terms (error 2^-16), far inside the rounding of the output. The adapters of
 // each 256-row tile and their masks come from a table built with low.
 #include "adapter.cuh"
 #include "ffn_args.cuh"
