@@ -195,14 +195,16 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
     }
   }
+  // TMEM is given back before the peers are waited for: one of them may be waiting for TMEM itself,
+  // beside another call's CTA that waits for a peer of its own
   tc_fence_before();
-  __syncwarp();
-  if (S > 1) cluster_sync();
-  else __syncthreads();
+  __syncthreads();
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, BN);
   }
+  __syncwarp();
+  if (S > 1) cluster_sync();
   // ---- this rank's tokens: the partial rows of all ranks in rank order, four columns a lane
   if (ok) {
     // a warp takes 32 / LANES rows at a time

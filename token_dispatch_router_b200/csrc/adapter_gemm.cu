@@ -31,7 +31,10 @@ constexpr int STAGE_BYTES = A_BYTES + B_HALF;  // 32 KB a CTA
 constexpr int THREADS = 192;                   // producer, MMA, 4 epilogue warps
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int SMEM_TAIL = 512;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SMEM_TAIL;
+// All that a CTA can have: it holds all of TMEM while it waits for the kernel before it, so no
+// CTA of another call that wants TMEM may come beside it.
+constexpr int SMEM_BYTES = 227 * 1024;
+static_assert(1024 + STAGES * STAGE_BYTES + SMEM_TAIL <= SMEM_BYTES, "ring and barriers");
 
 struct AdapterGemmArgs {
   int T, n_out, kblocks, mt, nt, rank;
@@ -116,8 +119,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // low and the table of tiles come from the kernel before this one; x, d_y, W and the adapters
   // are older (that kernel lets this one start only once all before it is complete). So only the
   // adapter term waits for it (backward, 300 rows: 23.7 us with the wait here, 19.8
-  // without). A CTA's shared memory leaves no room beside it for one of that kernel, whose TMEM it
-  // could otherwise hold up.
+  // without).
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {

@@ -281,13 +281,16 @@ __global__ void __launch_bounds__(THREADS)
       o[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
   }
+  // TMEM is given back before the peers are waited for: one of them may be waiting for TMEM itself,
+  // beside another call's CTA that waits for a peer of its own
   tc_fence_before();
-  __syncwarp();
-  cluster_sync();
+  __syncthreads();
   if (warp == 4) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, tcols);
   }
+  __syncwarp();
+  cluster_sync();
   // this rank's share of the rows: the four partials in rank order
   const float sc = g.scale[l];
   uint32_t peer[SPLIT];

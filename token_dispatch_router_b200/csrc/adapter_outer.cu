@@ -179,13 +179,14 @@ __global__ void __launch_bounds__(THREADS)
     s_abort = 0;
     mbar_init_fence();
   }
-  if (warp == 4) tmem_alloc<1>(saddr(&s_tmem), tcols);
   if (tid == 32) {
     prefetch_map(&tmP0);
     prefetch_map(&tmP1);
   }
   // early: the large product before this kernel waited for what both read, and wrote none of it
   if (!g.early) pdl_wait();  // the previous kernel in the stream has completed
+  // TMEM is taken after that wait: the previous kernel's CTAs may still be waiting for theirs
+  if (warp == 4) tmem_alloc<1>(saddr(&s_tmem), tcols);
   pdl_trigger();
   if (warp == 0) make_line(line, g);
   tc_fence_before();
