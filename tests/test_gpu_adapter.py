@@ -384,3 +384,36 @@ def test_a_decode_step_and_a_tuning_step(cuda_lib):
     for got, want in ((d_x, x.grad), (d_a, a.grad), (d_b, b.grad)):
         # bf16 roundings of h, the activations and the layer's input gradient: a few 2^-8
         assert ((got.double() - want).norm() / want.norm()) < 6 * BF16
+
+
+def test_many_calls_on_several_streams(cuda_lib):
+    """CTAs of several calls share SMs and their tensor memory, in pieces of several sizes: no call
+    may hold some of it while it waits for another call, and results stay what they are alone."""
+    tdr = cuda_lib
+    shapes = [(300, 1024, 768, 4, 8), (513, 2048, 1024, 8, 64), (700, 256, 512, 6, 128),
+              (2049, 960, 1024, 48, 24), (57, 1024, 960, 32, 16), (1500, 512, 512, 3, 16)]
+    sets, ref = [], []
+    for shape in shapes:
+        inp = make(*shape, shape[0], "runs")
+        s, (y, low, ws) = call_forward(tdr, inp)
+        sets.append((s, inp, low, [torch.empty_like(ws) for _ in range(4)]))
+        ref.append([t.clone() for t in (y, *backward(tdr, s, inp, low))])
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for turn in range(40):
+        got = []
+        for i in range(24):
+            k, j = (7 * i + turn) % len(sets), i % 4
+            s, inp, low, ws = sets[k]
+            with torch.cuda.stream(streams[j]):
+                y = call_forward(tdr, inp, workspace=ws[j])[1][0]
+                g = backward(tdr, s, inp, low, workspace=ws[j], want_d_x=(i + turn) % 3 > 0)
+                got.append((k, (y, *g)))
+        torch.cuda.synchronize()
+        for k, outs in got:
+            for a, b in zip(outs, ref[k]):
+                if a is not None:
+                    wrong += (a != b).any()
+        torch.cuda.synchronize()
+    assert wrong.item() == 0 and tdr.device_status() == 0
