@@ -1,6 +1,6 @@
 // Host side of the adapter products: workspace layouts and launch sequences.
 //
-//   forward,  at most 128 rows: low partials -> product with the adapter term (two launches)
+//   forward,  few rows:         low partials -> product with the adapter term (two launches)
 //   forward,  more rows:        group rows by adapter -> low -> product with the adapter term
 //   backward:                   group -> d_low -> d_x product with the adapter term
 //                               -> outer products d_A, d_B
@@ -46,6 +46,14 @@ moe_status launch_adapter_sum(const AdapterTileSums& a, const AdapterUnitSums& b
 namespace {
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Whether the forward takes the kernels for few rows: their adapter terms are sums of a row at a
+// time, so their time grows with rows times rank, while grouping costs three launches whatever the
+// size (512 -> 3584: 64 rows of rank 64, 29.6 us against 32.6 grouped; 97 rows, 47.0 against 33.4;
+// 2048 -> 2880: 28.5 against 41.0 and 45.7 against 41.4; 128 rows of rank 32: 29.2 against 37.7).
+bool few_rows(const moe_adapter_shape& s) {
+  return s.T <= kFewMaxTokens && s.T * s.rank <= 5120;
+}
 
 // Splits of the few-row low sums: two CTAs a SM over all rows, at least 64 of d_in each.
 int low_few_splits(const moe_adapter_shape& s) {
@@ -107,7 +115,7 @@ moe_status group(const moe_adapter_shape& s, const int32_t* ids, const Layout& L
 }  // namespace
 
 size_t adapter_forward_bytes(const moe_adapter_shape& s) {
-  return s.T <= kFewMaxTokens ? up256((size_t)low_few_splits(s) * s.T * s.rank * 4)
+  return few_rows(s) ? up256((size_t)low_few_splits(s) * s.T * s.rank * 4)
                               : layout(s).total_fwd;
 }
 size_t adapter_backward_bytes(const moe_adapter_shape& s) { return layout(s).total; }
@@ -117,7 +125,7 @@ moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, con
                                   const float* scale, float* low, void* y, uint8_t* ws,
                                   cudaStream_t st) {
   moe_status r;
-  if (s.T <= kFewMaxTokens) {
+  if (few_rows(s)) {
     AdapterFewArgs f = {};
     f.T = s.T;
     f.d = s.d_out;
