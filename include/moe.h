@@ -340,7 +340,8 @@ moe_status moe_decode(const moe_shape* shape, const void* x, const void* w_r, co
  *     d_x_t  = d_y_t W^T + d_low A[l]^T           (fp32 sums, rounded once to bf16)
  *     d_a[l] = sum over l's rows of x_t^T d_low,  d_b[l] = sum of low[t]^T d_y_t   (fp32)
  * Results repeat bit for bit. Adapters do not mix: an infinity or NaN of one adapter, or of
- * one row, stays in the rows (and, backward, the gradients) that it belongs to.
+ * one row, stays in the rows (and, backward, the gradients) that it belongs to, and gives the
+ * infinities and NaNs there that these formulas give.
  *
  *   x     [T, d_in]  w [d_in, d_out]  a [n_adapters, d_in, rank]  b [n_adapters, rank, d_out]
  *         device bf16

@@ -2,6 +2,8 @@
 // the split of an fp32 value into bf16 terms.
 #pragma once
 
+#include <math.h>
+
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -48,12 +50,37 @@ struct AdapterUnitSums {
   float* out[2];
 };
 
-// (a, b) as bf16 pairs hi + lo (+ what is left, returned in a and b): 8 bits of mantissa each.
-__device__ __forceinline__ uint32_t take_bf16x2(float& a, float& b) {
-  const uint32_t h = pack_bf16x2(a, b);
-  a -= __uint_as_float(h << 16);
-  b -= __uint_as_float(h & 0xffff0000u);
-  return h;
+// A value as N bf16 terms that add up to it: N = 2 to 2^-16 of it, N = 3 exactly (both above
+// 2^-100). Each term has the value's sign and none is zero unless the value is, so a product with
+// an infinity comes out as the value's own would, term by term (rounded terms leave a rest of the
+// other sign, or of zero: inf - inf, 0 inf). So bits are cut off rather than rounded, which leaves
+// the largest finite values finite, too; where nothing is left for a term, it shares the one before
+// (halves are exact); and an infinity or NaN is itself in every term.
+template <int N>
+__device__ __forceinline__ void bf16_terms(float v, float (&t)[N]) {
+  float rest = v;
+#pragma unroll
+  for (int i = 0; i < N - 1; ++i) {
+    t[i] = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+    rest -= t[i];
+  }
+  t[N - 1] = rest;  // rounded where it is packed
+#pragma unroll
+  for (int i = 1; i < N; ++i)
+    if (t[i] == 0.f && fabsf(t[i - 1]) >= 0x1p-120f) t[i] = t[i - 1] *= 0.5f;
+  if (!(fabsf(v) < INFINITY))
+#pragma unroll
+    for (int i = 0; i < N; ++i) t[i] = v;
+}
+
+// (a, b) as N packed pairs of such terms.
+template <int N>
+__device__ __forceinline__ void bf16x2_terms(float a, float b, uint32_t (&h)[N]) {
+  float s[N], t[N];
+  bf16_terms<N>(a, s);
+  bf16_terms<N>(b, t);
+#pragma unroll
+  for (int i = 0; i < N; ++i) h[i] = pack_bf16x2(s[i], t[i]);
 }
 
 }  // namespace moe

@@ -310,18 +310,20 @@ __global__ void __launch_bounds__(THREADS)
     v1 *= sc;
     const size_t o = (size_t)s_row[r] * g.r + j;
     *reinterpret_cast<float2*>(g.low + o) = make_float2(v0, v1);
-    {
-      float a0 = v0, a1 = v1;
-      *reinterpret_cast<uint32_t*>(g.terms + o) = take_bf16x2(a0, a1);
-      *reinterpret_cast<uint32_t*>(g.terms + (size_t)g.T * g.r + o) = pack_bf16x2(a0, a1);
-    }
+    uint32_t h[2];
+    bf16x2_terms<2>(v0, v1, h);
+    *reinterpret_cast<uint32_t*>(g.terms + o) = h[0];
+    *reinterpret_cast<uint32_t*>(g.terms + (size_t)g.T * g.r + o) = h[1];
     if (g.planes != nullptr) {
       const size_t slot = (size_t)(first + r) * g.r + j, plane = (size_t)g.T * g.r;
-      float2 w = *reinterpret_cast<const float2*>(g.low2 + o);
+      const float2 w = *reinterpret_cast<const float2*>(g.low2 + o);
+      uint32_t hv[3], hw[3];
+      bf16x2_terms<3>(v0, v1, hv);
+      bf16x2_terms<3>(w.x, w.y, hw);
 #pragma unroll
       for (int p = 0; p < 3; ++p) {
-        *reinterpret_cast<uint32_t*>(g.planes + p * plane + slot) = take_bf16x2(v0, v1);
-        *reinterpret_cast<uint32_t*>(g.planes2 + p * plane + slot) = take_bf16x2(w.x, w.y);
+        *reinterpret_cast<uint32_t*>(g.planes + p * plane + slot) = hv[p];
+        *reinterpret_cast<uint32_t*>(g.planes2 + p * plane + slot) = hw[p];
       }
     }
   }

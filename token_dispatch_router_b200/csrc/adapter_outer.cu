@@ -6,7 +6,7 @@
 // gathered by cp.async into the swizzled layout that the tensor cores read; both operands are
 // taken as they lie (a row is one k of the product: MN-major), so nothing is transposed. M is
 // the wide side (256 columns a unit, two accumulators), N the rank (16 ... 128), K the rows.
-// The low-rank side is fp32: it enters as three bf16 terms, exact to 2^-24; the tensor pipe has
+// The low-rank side is fp32: it enters as three bf16 terms, which hold it exactly; the tensor pipe has
 // the time (three MMAs of N = r for each 32 x 256 tile of wide rows). The tensor core cuts what
 // it adds to an accumulator off rather than rounding it, an error that grows with the number of
 // additions: the small second and third terms have an accumulator of their own, added to the
