@@ -188,9 +188,13 @@ __global__ void __launch_bounds__(THREADS)
   }
   // early: the large product before this kernel waited for what both read, and wrote none of it
   if (!g.early) pdl_wait();  // the previous kernel in the stream has completed
-  // TMEM is taken after that wait: the previous kernel's CTAs may still be waiting for theirs
-  if (warp == 4) tmem_alloc<1>(saddr(&s_tmem), tcols);
-  pdl_trigger();
+  // TMEM is taken after that wait (the previous kernel's CTAs may still be waiting for theirs), and
+  // the next kernel in the stream may start only then: one that takes TMEM before it waits for this
+  // kernel, beside this CTA, could hold what this CTA still needs.
+  if (warp == 4) {
+    tmem_alloc<1>(saddr(&s_tmem), tcols);
+    pdl_trigger();
+  }
   if (warp == 0) make_line(line, g);
   tc_fence_before();
   __syncthreads();
