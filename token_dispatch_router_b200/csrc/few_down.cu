@@ -119,10 +119,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int b0 = work ? cut.begin(blockIdx.x) : 0, b1 = work ? cut.begin(blockIdx.x + 1) : 0;
   const int at0 = line > 0 ? b0 % line : 0;  // of the first block, in its tile's line
 
+  // Nothing that a load warp issued is in flight after this (bounded). A stage is full once both
+  // warps' copies into it have landed; one that the other never issued runs out, too.
+  auto drain = [&](uint32_t issued, uint32_t par) {
+    if (lane == 0)
+      for (int s = 0; s < stages; ++s) {
+        if (!(issued & (1u << s))) continue;
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try(saddr(&t.full[s]), (par >> s) & 1u) && globaltimer_ns() - t0 < limit) {
+        }
+      }
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------ weights
     int tile = line > 0 ? b0 / line : 0, a = at0 / g.kb, k = at0 % g.kb, stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, issued_mask = 0, issued_par = 0;
     const uint64_t once = l2_policy_evict_first();  // read once: act stays in L2
     for (int b = b0; b < b1; ++b) {
       if (!mbar_wait_warp(saddr(&t.empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
@@ -133,6 +145,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                          t.m.act[a], fb, once);
       }
       __syncwarp();
+      issued_mask |= 1u << stage;
+      issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
       if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
@@ -145,12 +159,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-    if (lane == 0 && *abort_flag) {
-      // a wait ran out: give the copies in flight time to land (else the MMAs have read them)
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 1000000) {
-      }
-    }
+    drain(issued_mask, issued_par);
   } else if (warp == 1) {
     // ------------------------------------------------------------ rows of act
     // a lane copies 64 k of eight of the expert's tokens (what lies behind the last one fills
@@ -162,7 +171,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (work) enter();
     pdl_wait();  // act is complete
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, issued_mask = 0, issued_par = 0;
     for (int b = b0; b < b1; ++b) {
       if (!mbar_wait_warp(saddr(&t.empty[stage]), phase ^ 1u, abort_flag, g.status, limit)) break;
       const uint32_t fb = saddr(&t.full[stage]);
@@ -174,6 +183,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         (uint32_t)(grp * X_ROWS * 128),
                     &tmX, k * BK + piece * 64, a * g.T + grp * X_ROWS, fb);
       __syncwarp();
+      issued_mask |= 1u << stage;
+      issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
       if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
@@ -184,11 +195,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         enter();
       }
     }
-    if (lane == 0 && *abort_flag) {  // as above
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 1000000) {
-      }
-    }
+    drain(issued_mask, issued_par);
   } else if (warp == 2) {
     // ------------------------------------------------------------ MMA issuer
     // D fp32, A and B bf16, A MN-major (bit 15), B K-major, M = 128, N = the expert's tokens
