@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   constexpr int PITCH = BN + 4;     // floats per row of the partial tile
   constexpr int LANES = BN / 4;     // lanes on a row of it, four columns each
   extern __shared__ uint8_t smem_raw[];
+  // the ring (later the partial tile, 528 bytes a row: less than two stages), low, barriers
   uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   Tail& t = *reinterpret_cast<Tail*>(base + g.ring_bytes + g.low_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -184,8 +185,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (q * 32 < g.T) {
 #pragma unroll 1
       for (int c = 0; c < BN; c += 8) {
-        uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-        if (b0 < b1) tmem_ld8(tmem + (uint32_t)c + ((uint32_t)(q * 32) << 16), v);
+        uint32_t v[8];
+        tmem_ld8(tmem + (uint32_t)c + ((uint32_t)(q * 32) << 16), v);
         tmem_ld_wait();
         if (row < g.T) {
           uint4* o = reinterpret_cast<uint4*>(part + (size_t)row * PITCH + c);
@@ -250,23 +251,26 @@ template <int BN>
 moe_status run_bn(AdapterFewArgs a, int d_in, const void* x, const void* w, cudaStream_t st) {
   constexpr int BK = W_BYTES / (2 * BN), PIECES = BK / 64;
   a.kb = (d_in + BK - 1) / BK;
-  // The largest cluster of 4, 2 or 1 that leaves every CTA two stages and the whole grid resident
-  // at once: two CTAs an SM where two stages of each fit, else one.
+  // The largest cluster of 4, 2 or 1 with which the whole grid runs at once: two CTAs an SM where
+  // two stages of each fit beside the cluster's share of low, else one (16 SMs are left out: clusters
+  // stay inside a group of SMs). More tiles than SMs run one after another, without clusters.
   const int tiles = (a.d + BN - 1) / BN, sms = sm_count();
   a.stage_bytes = W_BYTES + PIECES * ((a.T + 7) / 8 * 1024);
-  int fixed = 1024 + (int)sizeof(Tail) + 8192;  // with a guess at low, for the choice
-  const int most = SMEM_TWO - fixed >= 2 * a.stage_bytes ? 2 * sms - 16 : sms - 16;
+  auto low_bytes = [&](int split) {
+    return ((a.T + split - 1) / split * a.rank * 4 + 15) / 16 * 16;
+  };
+  auto fixed = [&](int split) { return 1024 + (int)sizeof(Tail) + low_bytes(split); };
+  auto two = [&](int split) { return SMEM_TWO - fixed(split) >= 2 * a.stage_bytes; };
+  auto at_once = [&](int split) { return split * tiles <= (two(split) ? 2 : 1) * sms - 16; };
   a.split = 1;
-  while (a.split < 4 && 2 * a.split * tiles <= most && a.kb >= 4 * a.split) a.split *= 2;
-  a.low_bytes = ((a.T + a.split - 1) / a.split * a.rank * 4 + 15) / 16 * 16;
-  fixed = 1024 + (int)sizeof(Tail) + a.low_bytes;
-  a.stages = ((a.split * tiles <= sms - 16 ? SMEM_ONE : SMEM_TWO) - fixed) / a.stage_bytes;
+  for (int n = 2; n <= 4 && 2 * n <= a.kb; n *= 2)  // every CTA has two stages at least
+    if (at_once(n)) a.split = n;
+  a.low_bytes = low_bytes(a.split);
+  a.stages = ((a.split * tiles <= sms - 16 ? SMEM_ONE : SMEM_TWO) - fixed(a.split)) / a.stage_bytes;
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
-  if (a.stages < 2) a.stages = (SMEM_MAX - fixed) / a.stage_bytes >= 2 ? 2 : 1;
+  if (a.stages < 2) a.stages = 2;  // one CTA an SM then (low is 20 KB at most: they fit)
   a.ring_bytes = a.stages * a.stage_bytes;
-  const int part = (a.T * (BN + 4) * 4 + 1023) / 1024 * 1024;  // the partial tile takes its place
-  if (a.ring_bytes < part) a.ring_bytes = part;
-  const int smem = fixed + a.ring_bytes;
+  const int smem = fixed(a.split) + a.ring_bytes;
   a.status = device_status_ptr();
   a.limit_ns = kWaitLimitNs;
   CUtensorMap mx, mw;
