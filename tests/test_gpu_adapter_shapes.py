@@ -20,8 +20,10 @@ def check_forward(tdr, inp):
 
 
 @pytest.mark.parametrize("T,d_in,d_out,L,r", [
-    (64, 512, 32768, 5, 80), (40, 192, 20480, 3, 128), (71, 1088, 8448, 5, 32), (70, 1024, 16896, 5, 32),
-    (66, 1024, 16384, 8, 8), (33, 2048, 2880, 8, 72), (128, 64, 320, 2, 40), (127, 576, 17024, 9, 8),
+    (64, 512, 32768, 24, 80), (40, 192, 20480, 30, 128), (71, 1088, 8448, 5, 32),
+    (70, 1024, 16896, 5, 32), (66, 1024, 16384, 8, 8), (33, 2048, 2880, 8, 72), (128, 64, 320, 30, 40),
+    (127, 576, 17024, 9, 8), (128, 256, 192, 128, 128), (128, 2048, 1024, 128, 64),
+    (100, 1024, 640, 256, 120),
 ])
 def test_few_rows_through_wide_projections(cuda_lib, T, d_in, d_out, L, r):
     """Around the sizes where two CTAs no longer fit an SM, clusters shrink, tiles outnumber SMs."""

@@ -47,12 +47,22 @@ namespace {
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Whether the forward takes the kernels for few rows: their adapter terms are sums of a row at a
-// time, so their time grows with rows times rank, while grouping costs three launches whatever the
-// size (512 -> 3584: 64 rows of rank 64, 29.6 us against 32.6 grouped; 97 rows, 47.0 against 33.4;
-// 2048 -> 2880: 28.5 against 41.0 and 45.7 against 41.4; 128 rows of rank 32: 29.2 against 37.7).
+// Whether the forward takes the kernels for few rows. Their adapter terms are sums of a row at a
+// time: their time grows with rows times rank, whoever's rows they are. The grouped kernels pay for
+// every adapter that a tile's rows have (about 1 us, 2 at rank 128) and for three launches. How many
+// there are is not known here: as many as there can be. Measured, few rows / grouped, us, and the
+// limit's side (512 -> 3584, 2048 -> 2880, 4096 -> 4096):
+//   64 rows of rank 64, 4 adapters    30 / 20    28 / 27    35 / 30   grouped
+//   64 rows of rank 64, 32            30 / 50    29 / 59    36 / 69   few
+//   128 rows of rank 16, 1            20 / 18    19 / 22    24 / 25   few
+//   128 rows of rank 32, 16           31 / 31    30 / 38    37 / 45   few
+//   128 rows of rank 64, 32           51 / 53    49 / 60    64 / 70   grouped
+//   128 rows of rank 64, 128          67 / 166   60 / 193   95 / 203  few
+//   128 rows of rank 128, 128        147 / 334  135 / 359  177 / 372  few
 bool few_rows(const moe_adapter_shape& s) {
-  return s.T <= kFewMaxTokens && s.T * s.rank <= 5120;
+  if (s.T > kFewMaxTokens) return false;
+  const int most = s.n_adapters < s.T ? s.n_adapters : s.T;
+  return s.T * s.rank <= 2048 + 128 * most;
 }
 
 // Splits of the few-row low sums: two CTAs a SM over all rows, at least 64 of d_in each.

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   constexpr int PITCH = BN + 4;     // floats per row of the partial tile
   constexpr int LANES = BN / 4;     // lanes on a row of it, four columns each
   extern __shared__ uint8_t smem_raw[];
-  // the ring (later the partial tile, 528 bytes a row: less than two stages), low, barriers
+  // the ring (later the partial tile, at most 528 bytes a row: less than a ring), low, barriers
   uint8_t* base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   Tail& t = *reinterpret_cast<Tail*>(base + g.ring_bytes + g.low_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -268,7 +268,8 @@ moe_status run_bn(AdapterFewArgs a, int d_in, const void* x, const void* w, cuda
   a.low_bytes = low_bytes(a.split);
   a.stages = ((a.split * tiles <= sms - 16 ? SMEM_ONE : SMEM_TWO) - fixed(a.split)) / a.stage_bytes;
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
-  if (a.stages < 2) a.stages = 2;  // one CTA an SM then (low is 20 KB at most: they fit)
+  // one CTA an SM then; a single stage where low (64 KB at most) leaves no more
+  if (a.stages < 2) a.stages = SMEM_MAX - fixed(a.split) >= 2 * a.stage_bytes ? 2 : 1;
   a.ring_bytes = a.stages * a.stage_bytes;
   const int smem = fixed(a.split) + a.ring_bytes;
   a.status = device_status_ptr();
