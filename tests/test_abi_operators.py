@@ -101,3 +101,12 @@ def test_workspaces_grow_with_the_rows(lib):
     assert all(p > 0 for p in sizes) and sizes == sorted(sizes)
     sizes = [tdr.decode_workspace_size(tdr.make_shape(T, 2048, 64, 8, 1024)) for T in (0, 1, 8, 128)]
     assert all(p > 0 for p in sizes) and sizes == sorted(sizes)
+
+
+def test_the_table_of_tiles_has_room_for_the_adapters_there_are(lib):
+    """A 256-row tile lists at most n_adapters of them, 36 bytes each: 2^24 rows of one adapter do
+    without 255 of 256 in 65536 tiles."""
+    def size(n):
+        return tdr.adapter_workspace_size(tdr.make_adapter_shape(1 << 24, 64, 64, n, 8))
+
+    assert size(256) - size(1) >= 65536 * 252 * 36

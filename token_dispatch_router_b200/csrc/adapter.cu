@@ -25,9 +25,9 @@ moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void
                               const void* m, const int32_t* ids, const int32_t* offsets,
                               const int32_t* rows, const float* scale, float* low, void* planes,
                               const float* low2, void* planes2, void* terms,
-                              AdapterTile* tiles, cudaStream_t st);
+                              AdapterTiles tiles, cudaStream_t st);
 moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
-                               const void* in, const void* w, const AdapterTile* tiles,
+                               const void* in, const void* w, AdapterTiles tiles,
                                const void* low, const void* m, void* out, float* part,
                                cudaStream_t st);
 AdapterTileSums adapter_gemm_sums(int T, int k_dim, int n_out, void* out, const float* part);
@@ -101,7 +101,7 @@ Layout layout(const moe_adapter_shape& s) {
   L.a2p = take(T * 4);
   L.rows = take(T * 4);
   L.scratch = take(permute_scratch_bytes(group_shape(s)));
-  L.tiles = take((T + kAdapterTileRows - 1) / kAdapterTileRows * sizeof(AdapterTile));
+  L.tiles = take(AdapterTiles::bytes((s.T + kAdapterTileRows - 1) / kAdapterTileRows, s.n_adapters));
   L.terms = take(2 * T * r * 2);
   const size_t pf = adapter_gemm_part_bytes(s.T, s.d_in, s.d_out);
   const size_t pb = adapter_gemm_part_bytes(s.T, s.d_out, s.d_in);
@@ -113,6 +113,10 @@ Layout layout(const moe_adapter_shape& s) {
   L.part = take(adapter_outer_part_bytes(s.T, s.rank));
   L.total = o;
   return L;
+}
+
+AdapterTiles tiles_at(const moe_adapter_shape& s, const Layout& L, uint8_t* ws) {
+  return AdapterTiles{(int32_t*)(ws + L.tiles), AdapterTiles::most_of(s.n_adapters)};
 }
 
 moe_status group(const moe_adapter_shape& s, const int32_t* ids, const Layout& L, uint8_t* ws,
@@ -158,11 +162,11 @@ moe_status launch_adapter_forward(const moe_adapter_shape& s, const void* x, con
   if ((r = launch_adapter_low(false, s.T, s.d_in, s.rank, s.n_adapters, x, a, ids,
                               (const int32_t*)(ws + L.offsets), (const int32_t*)(ws + L.rows),
                               scale, low, nullptr, nullptr, nullptr, ws + L.terms,
-                              (AdapterTile*)(ws + L.tiles), st)) != MOE_OK)
+                              tiles_at(s, L, ws), st)) != MOE_OK)
     return r;
   float* part = (float*)(ws + L.gemm_part);
   if ((r = launch_adapter_gemm(false, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, x, w,
-                               (const AdapterTile*)(ws + L.tiles), ws + L.terms, b, y, part,
+                               tiles_at(s, L, ws), ws + L.terms, b, y, part,
                                st)) != MOE_OK)
     return r;
   return launch_adapter_sum(adapter_gemm_sums(s.T, s.d_in, s.d_out, y, part), AdapterUnitSums{},
@@ -182,14 +186,14 @@ moe_status launch_adapter_backward(const moe_adapter_shape& s, const void* d_y, 
   if ((r = group(s, ids, L, ws, st)) != MOE_OK) return r;
   if ((r = launch_adapter_low(
            true, s.T, s.d_out, s.rank, s.n_adapters, d_y, b, ids, offsets, rows, scale, d_low,
-           ws + L.planes_d, low, ws + L.planes_l, ws + L.terms, (AdapterTile*)(ws + L.tiles),
+           ws + L.planes_d, low, ws + L.planes_l, ws + L.terms, tiles_at(s, L, ws),
            st)) != MOE_OK)
     return r;
   float* gemm_part = (float*)(ws + L.gemm_part);
   float* part = (float*)(ws + L.part);
   if (d_x != nullptr &&
       (r = launch_adapter_gemm(true, s.T, s.d_in, s.d_out, s.n_adapters, s.rank, d_y, w,
-                               (const AdapterTile*)(ws + L.tiles), ws + L.terms, a, d_x,
+                               tiles_at(s, L, ws), ws + L.terms, a, d_x,
                                gemm_part, st)) != MOE_OK)
     return r;
   // the outer products start as the large product's CTAs leave; what both leave is added last

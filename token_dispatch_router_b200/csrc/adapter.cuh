@@ -8,14 +8,26 @@
 
 namespace moe {
 
-// The adapters that have rows in a 256-row tile of the large product, and for each the rows
-// (bit r % 32 of word r / 32) that are NOT its own.
+// The table of the large product's 256-row tiles. For each: how many adapters have rows in it, which
+// ones, and for each of them the rows (bit r % 32 of word r / 32) that are NOT its own. A tile has
+// room for as many as there can be, so that 2^24 rows of one adapter take 10 MB and not 605.
 constexpr int kAdapterTileRows = 256;
-struct AdapterTile {
-  int n;
-  int pad[3];
-  int id[kAdapterTileRows];
-  uint32_t off[kAdapterTileRows][8];
+struct AdapterTiles {
+  int32_t* at;
+  int most;  // adapters of a tile at most, rounded up to 4: words of a tile stay 16-byte aligned
+  __host__ __device__ static int most_of(int n_adapters) {
+    return ((n_adapters < kAdapterTileRows ? n_adapters : kAdapterTileRows) + 3) / 4 * 4;
+  }
+  __host__ __device__ static size_t bytes(int n_tiles, int n_adapters) {
+    return (size_t)n_tiles * (4 + 9 * most_of(n_adapters)) * 4;
+  }
+  __device__ __forceinline__ int32_t* count(int m) const {
+    return at + (size_t)m * (4 + 9 * most);
+  }
+  __device__ __forceinline__ int32_t* ids(int m) const { return count(m) + 4; }
+  __device__ __forceinline__ uint32_t* off(int m, int i) const {
+    return reinterpret_cast<uint32_t*>(ids(m) + most + 8 * i);
+  }
 };
 
 // Tile w of the large product: kAdapterTileGroup row tiles at a time, all column tiles of the

@@ -40,7 +40,7 @@ struct AdapterGemmArgs {
   int T, n_out, kblocks, mt, nt, rank;
   int whole, split;          // tiles made whole; pairs that share the contraction of the others
   float* part;               // [others][split][2 CTAs][64][128 rows][4]
-  const AdapterTile* tiles;  // [mt]
+  AdapterTiles tiles;        // [mt]
   bf16* out;                 // [T, n_out]
   unsigned* status;
   unsigned long long limit_ns;
@@ -167,8 +167,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           pdl_trigger();
           waited = true;
         }
-        const AdapterTile* at = g.tiles + m;
-        const int n_ad = it.adapters ? at->n : 0;
+        const int n_ad = it.adapters ? *g.tiles.count(m) : 0;
         for (int i = 0; i < n_ad && ok; ++i) {
           if (i % group == 0)
             for (int j = 0; j < nl; ++j) {
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               tma_load_3d_pair(a, &tmLow, 64 * j, m0, 0, fb);
               tma_load_3d_pair(a + A_BYTES, &tmLow, 64 * j, m0, 1, fb);
             }
-          const int l = at->id[i];
+          const int l = g.tiles.ids(m)[i];
           for (int j = 0; j < nl && ok; ++j) {
             if (!begin(B_HALF, fb, a)) break;
             const uint32_t b = a + A_BYTES;
@@ -249,13 +248,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!waited) pdl_wait();  // the previous kernel in the stream has completed
         waited = true;
-        const AdapterTile* at = g.tiles + m;
-        const int n_ad = wi.adapters ? at->n : 0;
+        const int n_ad = wi.adapters ? *g.tiles.count(m) : 0;
         int low[2] = {0, 0};
         for (int i = 0; i < n_ad && ok; ++i) {
           uint32_t off[8];
           {
-            const uint4* mp = reinterpret_cast<const uint4*>(at->off[i]);
+            const uint4* mp = reinterpret_cast<const uint4*>(g.tiles.off(m, i));
             const uint4 u = mp[0], v = mp[1];
             off[0] = u.x; off[1] = u.y; off[2] = u.z; off[3] = u.w;
             off[4] = v.x; off[5] = v.y; off[6] = v.z; off[7] = v.w;
@@ -402,7 +400,7 @@ size_t adapter_gemm_part_bytes(int T, int k_dim, int n_out) {
 // in [T, k_dim], w [d_in, d_out]; forward: k_dim = d_in, out [T, d_out], m = B; backward:
 // k_dim = d_out, out [T, d_in], m = A. low: [2][T][rank] bf16 terms.
 moe_status launch_adapter_gemm(bool bwd, int T, int d_in, int d_out, int n_adapters, int rank,
-                               const void* in, const void* w, const AdapterTile* tiles,
+                               const void* in, const void* w, AdapterTiles tiles,
                                const void* low, const void* m, void* out, float* part,
                                cudaStream_t st) {
   const int k_dim = bwd ? d_out : d_in, n_out = bwd ? d_in : d_out;

@@ -40,7 +40,7 @@ struct LowArgs {
   const float* low2;  // with planes: another [T, r] ...
   bf16* planes2;      // ... put into slot order the same way
   bf16* terms;        // [2][T][r]: low as two bf16 terms
-  AdapterTile* tiles; // [ceil(T / 256)]
+  AdapterTiles tiles; // [ceil(T / 256)]
   int tile_clusters;  // clusters up to here make low, those behind the table of tiles
   int T, D, r, L;
   int n_mma, nc;      // the rank rounded up to 16; its 64-wide pieces
@@ -85,7 +85,7 @@ __device__ __forceinline__ void make_tile(int m, const LowArgs& g, uint8_t* smem
   }
   __syncthreads();
   if (tid >= 32) return;
-  AdapterTile* t = g.tiles + m;
+  int32_t* ids = g.tiles.ids(m);
   int n = 0;
   for (int l0 = 0; l0 < g.L; l0 += 32) {
     const int l = l0 + lane;
@@ -96,13 +96,14 @@ __device__ __forceinline__ void make_tile(int m, const LowArgs& g, uint8_t* smem
     const unsigned has = __ballot_sync(0xffffffffu, any != 0u);
     if (any != 0u) {
       const int at = n + __popc(has & lanemask_lt());
-      t->id[at] = l;
+      ids[at] = l;
+      uint32_t* off = g.tiles.off(m, at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t->off[at][i] = ~own[l * 8 + i];
+      for (int i = 0; i < 8; ++i) off[i] = ~own[l * 8 + i];
     }
     n += __popc(has);
   }
-  if (lane == 0) t->n = n;
+  if (lane == 0) *g.tiles.count(m) = n;
 }
 
 // TRANS: the adapter's matrix is [r, D] (the backward's B_l), else [D, r].
@@ -428,7 +429,7 @@ moe_status launch_adapter_low(bool trans, int T, int D, int r, int L, const void
                               const void* m, const int32_t* ids, const int32_t* offsets,
                               const int32_t* rows, const float* scale, float* low, void* planes,
                               const float* low2, void* planes2, void* terms,
-                              AdapterTile* tiles, cudaStream_t st) {
+                              AdapterTiles tiles, cudaStream_t st) {
   LowArgs a = {};
   a.in = (const bf16*)in;
   a.ids = ids;
