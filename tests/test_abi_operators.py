@@ -110,3 +110,17 @@ def test_the_table_of_tiles_has_room_for_the_adapters_there_are(lib):
         return tdr.adapter_workspace_size(tdr.make_adapter_shape(1 << 24, 64, 64, n, 8))
 
     assert size(256) - size(1) >= 65536 * 252 * 36
+
+
+def test_the_stream_of_a_call_without_torchs_own_shortcut(monkeypatch):
+    """Every call passes the current stream's handle; the shortcut to it may go from torch."""
+    import importlib.util
+    import types
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("tdr_without_shortcut", tdr.__file__)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=77))
+    assert mod._stream() == 77

@@ -157,9 +157,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# The handle alone: torch.cuda.current_stream() makes a stream object first, 3 us of a call. The
+# function is not part of torch's public interface; without it the stream object gives the handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream() -> int:
-    # the handle alone: torch.cuda.current_stream() makes a stream object first, 3 us of a call
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> None:
