@@ -65,9 +65,9 @@ bool few_rows(const moe_adapter_shape& s) {
   return s.T * s.rank <= 2048 + 128 * most;
 }
 
-// Splits of the few-row low sums: two CTAs a SM over all rows, at least 64 of d_in each.
+// Splits of the few-row low sums: two CTAs an SM over all rows, at least 64 of d_in each, 16 at most.
 int low_few_splits(const moe_adapter_shape& s) {
-  int n = 2 * 148 / (s.T > 0 ? s.T : 1);
+  int n = 2 * sm_count() / (s.T > 0 ? s.T : 1);
   if (n > s.d_in / 64) n = s.d_in / 64;
   return n < 1 ? 1 : n > 16 ? 16 : n;
 }
