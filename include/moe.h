@@ -315,6 +315,9 @@ moe_status moe_forward_workspace_layout(const moe_shape* shape, moe_workspace_la
  * Arguments, ties, renormalize, bias, logits_in and capacity_factor as moe_forward; a row of
  * x or logits that is NaN, or logits that are all -inf, give a NaN row and touch no other.
  * Results repeat bit for bit. ffn_variant and route_topk do not apply.
+ * Up to 128 tokens it takes less time than moe_forward (1 token, 2 of 8 experts of 14336, width
+ * 4096: 118 us against 295; 128 tokens: 487 against 535 or more), except in layers of a few MB (8
+ * experts of 512, width 256), where moe_forward is as fast from 100 tokens on.
  * bf16 only; T <= MOE_DECODE_MAX_TOKENS; no tile_round: else MOE_ERR_UNSUPPORTED.
  * x, w_r, w_gate, w_up, w_down and out 16-byte aligned, workspace 256-byte aligned and
  * >= moe_decode_workspace_size(shape) as given on the device that runs the call; nothing in it

@@ -14,7 +14,7 @@
 // read the accumulator and add up the partials. A finished wait costs a warp about 200 cycles
 // and a copy or an MMA 60 to issue, so a stage holds 32 KB of weights (128 or 256 k) brought by
 // one copy, and rows have a warp of their own.
-// Every wait is bounded (MOE_ERR_TIMEOUT on expiry).
+// Every wait (but tmem_alloc's) is bounded (MOE_ERR_TIMEOUT on expiry).
 #include "few.cuh"
 #include "few_args.cuh"
 #include "ffn_args.cuh"

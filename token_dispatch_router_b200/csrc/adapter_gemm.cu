@@ -5,15 +5,18 @@
 //
 // The large product runs on CTA pairs (tcgen05.mma.cta_group::2, 256 x 256 tiles, TMA-fed,
 // accumulators double-buffered in TMEM); W is read as it lies, MN-major forward and K-major
-// backward. Bound by the tensor pipe.
+// backward. Bound by the tensor pipe while a tile's rows have few adapters.
 //
 // The adapter term is a few more k-blocks of the same accumulation: after a tile's product, for
 // each adapter that has rows in the tile, low (A operand) times the adapter's matrix (B operand),
 // with the MMA's lane mask (disable-output-lane) keeping it out of the other rows. Rows of one
 // tile may so belong to any adapters in any order, nothing is multiplied by zero (an infinity
 // or NaN in one adapter stays in its own rows), and the epilogue only stores. low is fp32: it
-// enters as two bf16 terms (error 2^-16), far inside the rounding of the output. The adapters of
-// each 256-row tile and their masks come from a table built with low.
+// enters as two bf16 terms (bf16_terms, error 2^-16), far inside the rounding of the output. The
+// adapters of each 256-row tile and their masks come from a table built with low. Every adapter of a
+// tile costs a stage and its MMAs over all of the tile's rows, and the low of every four (two above
+// rank 64) is loaded again: rows with an adapter each are bound by that (forward, 4096 -> 4096, rank
+// 16, one adapter and one a row: 129 rows 31 and 157 us, 256 rows 39 and 286, 512 rows 46 and 287).
 #include "adapter.cuh"
 #include "ffn_args.cuh"
 

@@ -6,8 +6,8 @@
 // gathered by cp.async into the swizzled layout that the tensor cores read; both operands are
 // taken as they lie (a row is one k of the product: MN-major), so nothing is transposed. M is
 // the wide side (256 columns a unit, two accumulators), N the rank (16 ... 128), K the rows.
-// The low-rank side is fp32: it enters as three bf16 terms, which hold it exactly; the tensor pipe has
-// the time (three MMAs of N = r for each 32 x 256 tile of wide rows). The tensor core cuts what
+// The low-rank side is fp32: it enters as three bf16 terms, which hold it exactly (bf16_terms); the
+// tensor pipe has the time (three MMAs of N = r for each 32 x 256 tile of wide rows). The tensor core cuts what
 // it adds to an accumulator off rather than rounding it, an error that grows with the number of
 // additions: the small second and third terms have an accumulator of their own, added to the
 // first's at the end (512 rows, relative to the gradient: 1.7e-6 in one accumulator, 0.5e-6 in two).
@@ -27,7 +27,7 @@
 // What bounds it is latency: 8192 rows as above take a CTA 37 us for 23 steps, neither fewer
 // copies nor a third of the MMAs change the call by more than 2 %, and six stages for one CTA an
 // SM take as long as three for two. The stores of a unit are 14 us of the call's 284.
-// Every wait is bounded (MOE_ERR_TIMEOUT on expiry).
+// Every wait (but tmem_alloc's) is bounded (MOE_ERR_TIMEOUT on expiry).
 #include "adapter.cuh"
 #include "few.cuh"
 #include "ffn_args.cuh"

@@ -18,11 +18,11 @@
 // it waits for that kernel (its launch follows that kernel's own wait, so everything older, the
 // ids among it, is complete).
 // Roles (256 threads): warp 0 copies weights, warp 1 the expert's rows of act, eight a copy (two
-// warps with cp.async: 30 us of 515 at 128 tokens, width 4096, 8 experts of 14336), warp 2 issues the MMAs (two accumulators, so that one is added while the next is
-// made), warps 4-7 add and store. A finished wait costs a warp about 200 cycles and a copy or an
+// warps with cp.async: 30 us of 515 at 128 tokens, width 4096, 8 experts of 14336), warp 2 issues
+// the MMAs (two accumulators, so that one is added while the next is made), warps 4-7 add and store. A finished wait costs a warp about 200 cycles and a copy or an
 // MMA 60 to issue, so a stage is 128 k of 128 columns, 32 KB brought by one copy and taken by
 // eight MMAs.
-// Every wait is bounded (MOE_ERR_TIMEOUT on expiry).
+// Every wait (but tmem_alloc's) is bounded (MOE_ERR_TIMEOUT on expiry).
 #include <math.h>
 
 #include "few.cuh"

@@ -1,7 +1,10 @@
 // First expert product of the few-token layer: for each expert e that keeps a token,
 //   act[a, j] = w[t, e] silu(x_t W_gate[e]) * (x_t W_up[e])      (a: e's place among them)
-// for its tokens t (t its j-th one), at most 128 of them. w is the routing weight: the second product then only
-// adds up.
+// for its tokens t (t its j-th one), at most 128 of them. w is the routing weight: the second
+// product then only adds up. Everything is fp32 up to act, which is rounded to bf16, the type that
+// the second product's MMA takes (at most 2^-8 of each value; the layer's output is 2.3e-3 from the
+// exact one in the mean, 1.7e-3 of which its own rounding alone makes). Two bf16 terms of act would
+// take that away, for twice the second product's rows and MMAs; moe_forward rounds here, too.
 //
 // Bound by reading W_gate and W_up of those experts. They are the MMA's A operand, 128 columns
 // of each on M (MN-major: a box goes by TMA from where it lies into shared memory and into the
@@ -17,8 +20,8 @@
 // Roles (256 threads): warp 0 copies the weights, warp 2 the rows of x (a copy takes its warp
 // about 60 cycles to issue, a finished wait 200: one warp for both was the bound), warp 1 issues
 // the MMAs (two accumulators, double-buffered), warps 4-7 read them (lane = weight column, column
-// = token). Every wait is bounded; on expiry
-// the status word records MOE_ERR_TIMEOUT and the CTA ends after its copies and MMAs in flight.
+// = token). Every wait (but tmem_alloc's) is bounded; on expiry the status word records
+// MOE_ERR_TIMEOUT and the CTA ends after its copies and MMAs in flight.
 #include <type_traits>
 
 #include "few.cuh"

@@ -234,6 +234,12 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
                      bar)
                  : "memory");
 }
+// Waits until the SM has `ncols` columns in one piece, the only wait here without a limit: the
+// instruction has no other form. CTAs that share SMs, of any stream's calls, must not wait for each
+// other through it, so a kernel that holds TMEM while it waits for another kernel leaves no shared
+// memory for another user of TMEM beside it, or waits for one that has all of its own (the next
+// kernel may start only once every CTA has allocated) or uses none; and none is held while a
+// cluster's peers, which may still wait for theirs, are waited for.
 template <int CTA_GROUP>
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   if (CTA_GROUP == 1) {
